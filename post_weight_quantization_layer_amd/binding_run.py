@@ -1,0 +1,242 @@
+"""ctypes binding of the calls of gptq_run.h (argument marshalling only), and
+the buffers the classes on top of them share.
+
+As in ``binding``: every function has the name of the C entry point it wraps,
+tensors become device pointers, the current torch stream (or ``stream``) a
+hipStream_t, a status that is not OK an exception.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import binding as B
+
+GPTQ_DT_F16 = 2
+GPTQ_NORM_NONE, GPTQ_NORM_RMS, GPTQ_NORM_LAYER = range(3)
+NORMS = {None: GPTQ_NORM_NONE, "none": GPTQ_NORM_NONE, "rms": GPTQ_NORM_RMS,
+         "layer": GPTQ_NORM_LAYER}
+DTYPES = {torch.float32: B.GPTQ_DT_F32, torch.bfloat16: B.GPTQ_DT_BF16,
+          torch.float16: GPTQ_DT_F16}
+
+EXPORTED = (
+    "gptq_tokens_ld", "gptq_quantize_tokens", "gptq_silu_mul_quantize",
+    "gptq_w8a8_layer_bytes", "gptq_w8a8_prepare", "gptq_w8a8_gemm_ws_bytes",
+    "gptq_w8a8_linear_ws_bytes", "gptq_w8a8_gemm", "gptq_w8a8_linear",
+    "gptq_norm_block", "gptq_token_logprobs_ws_bytes", "gptq_token_logprobs",
+)
+
+
+class gptq_w8a8_layer(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("rows_pad", ctypes.c_int64), ("k_pad", ctypes.c_int64),
+                ("mem", ctypes.c_void_p), ("mem_bytes", ctypes.c_size_t)]
+
+
+class gptq_norm_params(ctypes.Structure):
+    _fields_ = [("post", ctypes.c_int32), ("pre", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("block_scale", ctypes.c_float),
+                ("post_weight", ctypes.c_void_p), ("post_bias", ctypes.c_void_p),
+                ("pre_weight", ctypes.c_void_p), ("pre_bias", ctypes.c_void_p)]
+
+
+_lib = None
+
+
+def lib() -> ctypes.CDLL:
+    global _lib
+    if _lib is not None:
+        return _lib
+    L = B.lib()
+    P, I64, I32, SZ, F = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t,
+                          ctypes.c_float)
+    layer = ctypes.POINTER(gptq_w8a8_layer)
+    for name, res, args in (
+            ("gptq_tokens_ld", I64, [I64]),
+            ("gptq_quantize_tokens", I32, [P, I32, I64, I64, I64, P, I64, P, P, P]),
+            ("gptq_silu_mul_quantize", I32, [P, P, I32, I64, I64, I64, P, I64, P, P, P]),
+            ("gptq_w8a8_layer_bytes", SZ, [I64, I64]),
+            ("gptq_w8a8_prepare", I32, [P, P, P, I64, I64, P, SZ, layer, P]),
+            ("gptq_w8a8_gemm_ws_bytes", SZ, [layer, I64]),
+            ("gptq_w8a8_linear_ws_bytes", SZ, [layer, I64]),
+            ("gptq_w8a8_gemm", I32, [layer, P, I64, P, P, I64, P, I32, I64, P, SZ, P]),
+            ("gptq_w8a8_linear", I32, [layer, P, I32, I64, I64, P, I32, I64, P, SZ, P]),
+            ("gptq_norm_block", I32, [ctypes.POINTER(gptq_norm_params), I32, I64, I64, P, I64, P,
+                                      I64, P, I64, I64, P, I64, P, I64, P, I64, P, P, P]),
+            ("gptq_token_logprobs_ws_bytes", SZ, [I64, I64, I32]),
+            ("gptq_token_logprobs", I32, [P, I32, I64, I64, I64, P, F, I32, P, P, P, P, P, P, SZ,
+                                          P])):
+        f = getattr(L, name)
+        f.restype, f.argtypes = res, args
+    _lib = L
+    return L
+
+
+def _check(status: int):
+    if status != B.GPTQ_OK:
+        B._check(status)
+
+
+def _dtype(t: torch.Tensor, what: str) -> int:
+    try:
+        return DTYPES[t.dtype]
+    except KeyError:
+        raise TypeError(f"{what} must be float32, bfloat16 or float16, not {t.dtype}") from None
+
+
+def stream_ptr(stream=None) -> int:
+    return torch.cuda.current_stream().cuda_stream if stream is None else \
+        getattr(stream, "cuda_stream", stream)
+
+
+def matrix(t: torch.Tensor, what: str, rows: int | None = None, cols: int | None = None):
+    """A device matrix whose rows are contiguous, of the given size where one is given."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be a matrix with contiguous rows, got shape "
+                         f"{tuple(t.shape)} and strides {t.stride()}")
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{what} must be {'*' if rows is None else rows} x "
+                         f"{'*' if cols is None else cols}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on the GPU")
+    return t
+
+
+def ld(t: torch.Tensor) -> int:
+    """Row stride; a single row's is its length (torch may report any)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def vector(t: torch.Tensor, what: str, n: int, dtype: torch.dtype | None = None):
+    if t.numel() != n or not t.is_contiguous() or not t.is_cuda or \
+            (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what} must be {n} contiguous values on the GPU"
+                         + (f" of {dtype}" if dtype is not None else ""))
+    return t
+
+
+@contextlib.contextmanager
+def on(stream):
+    """Allocations inside belong to ``stream`` (None: the current one)."""
+    if stream is None:
+        yield
+        return
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(s):
+        yield
+
+
+class Scratch:
+    """Workspace of an object, one per stream that uses it, so that calls on
+    several streams do not share one; grows to the largest request."""
+
+    def __init__(self, device):
+        self.device = device
+        self._by_stream: dict[int, torch.Tensor] = {}
+
+    def __call__(self, nbytes: int, ptr: int, stream=None) -> int | None:
+        """Address of at least ``nbytes`` bytes for use on the stream at ``ptr``."""
+        if nbytes == 0:
+            return None
+        t = self._by_stream.get(ptr)
+        if t is None or t.numel() < nbytes:
+            with on(stream):
+                t = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            self._by_stream[ptr] = t
+        return t.data_ptr()
+
+
+def gptq_tokens_ld(cols: int) -> int:
+    n = lib().gptq_tokens_ld(cols)
+    if n == 0:
+        raise B.GptqError(B.GPTQ_ERR_INVALID_ARG, "cols must be in [1, 65536]")
+    return n
+
+
+def gptq_quantize_tokens(x, codes, scale, sum, stream=None):
+    """x tokens x cols float; codes tokens x ld int8; scale, sum: tokens float32 / int32."""
+    t, c = x.shape
+    _check(lib().gptq_quantize_tokens(x.data_ptr(), _dtype(x, "x"), t, c, ld(x), codes.data_ptr(),
+                                      ld(codes), scale.data_ptr(), sum.data_ptr(),
+                                      stream_ptr(stream)))
+
+
+def gptq_silu_mul_quantize(g, u, codes, scale, sum, stream=None):
+    """g, u tokens x cols of one type and row stride."""
+    t, c = g.shape
+    if u.dtype != g.dtype or u.shape != g.shape or ld(u) != ld(g):
+        raise ValueError("g and u must have one shape, type and row stride")
+    _check(lib().gptq_silu_mul_quantize(g.data_ptr(), u.data_ptr(), _dtype(g, "g"), t, c, ld(g),
+                                        codes.data_ptr(), ld(codes), scale.data_ptr(),
+                                        sum.data_ptr(), stream_ptr(stream)))
+
+
+def gptq_w8a8_layer_bytes(rows: int, cols: int) -> int:
+    n = lib().gptq_w8a8_layer_bytes(rows, cols)
+    if n == 0:
+        raise B.GptqError(B.GPTQ_ERR_INVALID_ARG,
+                          "rows and cols must be in [1, 2^24] x [1, 65536]")
+    return n
+
+
+def gptq_w8a8_prepare(q, scale, zero, mem, stream=None) -> gptq_w8a8_layer:
+    """``mem`` must stay alive as long as the returned layer is used."""
+    rows, cols = q.shape
+    layer = gptq_w8a8_layer()
+    _check(lib().gptq_w8a8_prepare(q.data_ptr(), scale.data_ptr(), zero.data_ptr(), rows, cols,
+                                   mem.data_ptr(), mem.numel() * mem.element_size(),
+                                   ctypes.byref(layer), stream_ptr(stream)))
+    return layer
+
+
+def gptq_w8a8_gemm_ws_bytes(layer: gptq_w8a8_layer, tokens: int) -> int:
+    return lib().gptq_w8a8_gemm_ws_bytes(layer, tokens)
+
+
+def gptq_w8a8_linear_ws_bytes(layer: gptq_w8a8_layer, tokens: int) -> int:
+    return lib().gptq_w8a8_linear_ws_bytes(layer, tokens)
+
+
+def gptq_w8a8_gemm(layer: gptq_w8a8_layer, codes, scale, sum, y, ws=None, tokens=None,
+                   stream=None):
+    n = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().gptq_w8a8_gemm(layer, codes.data_ptr(), ld(codes), scale.data_ptr(),
+                                sum.data_ptr(), y.shape[0] if tokens is None else tokens,
+                                y.data_ptr(), _dtype(y, "y"), ld(y),
+                                None if ws is None else ws.data_ptr(), n, stream_ptr(stream)))
+
+
+def gptq_w8a8_linear(layer: gptq_w8a8_layer, x, y, ws=None, stream=None):
+    n = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().gptq_w8a8_linear(layer, x.data_ptr(), _dtype(x, "x"), ld(x), x.shape[0],
+                                  y.data_ptr(), _dtype(y, "y"), ld(y),
+                                  None if ws is None else ws.data_ptr(), n, stream_ptr(stream)))
+
+
+def gptq_norm_block(params: gptq_norm_params, r, b=None, gate=None, gate_tokens: int = 1,
+                    r_out=None, h=None, codes=None, scale=None, sum=None, stream=None):
+    t, d = r.shape
+
+    def at(x):
+        return (None, 0) if x is None else (x.data_ptr(), ld(x))
+
+    _check(lib().gptq_norm_block(params, _dtype(r, "r"), t, d, *at(r), *at(b), *at(gate),
+                                 gate_tokens, *at(r_out), *at(h), *at(codes),
+                                 B._ptr(scale), B._ptr(sum), stream_ptr(stream)))
+
+
+def gptq_token_logprobs_ws_bytes(rows: int, vocab: int, top_k: int) -> int:
+    return lib().gptq_token_logprobs_ws_bytes(rows, vocab, top_k)
+
+
+def gptq_token_logprobs(logits, ids, scale, top_k, logprob, rank, entropy, top_ids=None,
+                        top_logprobs=None, ws=None, stream=None):
+    rows, vocab = logits.shape
+    n = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().gptq_token_logprobs(
+        logits.data_ptr(), _dtype(logits, "logits"), rows, vocab, ld(logits), B._ptr(ids), scale,
+        top_k, B._ptr(logprob), B._ptr(rank), B._ptr(entropy), B._ptr(top_ids),
+        B._ptr(top_logprobs), B._ptr(ws), n, stream_ptr(stream)))

@@ -1,0 +1,548 @@
+// Log probabilities of given tokens, entropy and top alternatives from rows
+// of logits, in one pass over the logits.
+//
+// Every lane keeps a running maximum m of its logits, s = sum e^(z - m) and
+// t = sum (z - m) e^(z - m) (in powers of two); lanes, waves and, when a row
+// is split over workgroups, parts are joined by rescaling to the common
+// maximum.  Then ln p = scale (l - m) - ln s and the entropy is
+// ln s - t / s.
+//
+// Alternatives: each wave keeps a short list of candidates in LDS, every
+// logit above a threshold that k logits of the wave are known to reach.  The
+// first tile's threshold is the k-th largest of the wave's 256 maxima over 8
+// logits; whenever the list grows past a few k it is cut to its k best,
+// whose smallest is the new threshold.  So after the first tile almost every
+// tile costs one comparison per lane.  All selections go by (value, lower
+// index), so the result does not depend on the order of the work.
+#include <algorithm>
+
+#include "rows.h"
+
+namespace gptq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kChunkElems = 8 * kThreads;   // elements a workgroup takes per chunk
+constexpr int kUnroll = 4;                  // chunks per tile
+constexpr int kMaxTop = 64;
+// A wave's list takes a whole chunk (512) on top of k cut entries.
+constexpr int kListCap = 512 + kMaxTop;
+
+struct ScoreArgs {
+  const void *logits;
+  const int64_t *ids;
+  int64_t ld;
+  int vocab, k, splits, seg;    // seg: elements per split (a multiple of kChunkElems)
+  float scale;
+  float *logprob;
+  int *rank;
+  float *entropy;
+  int *top_ids;
+  float *top_logprobs;
+  float *part;                  // splits > 1: per (row, split) kPartWords words
+  uint64_t *part_keys;          //             and k keys
+};
+constexpr int kPartWords = 4;   // m, s, t, rank count
+
+// Floats as integers of the same order; -0 and +0 are equal.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return b ^ (uint32_t(int32_t(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t o) {
+  return __uint_as_float(o ^ (uint32_t(int32_t(~o) >> 31) | 0x80000000u));
+}
+// Largest float below v (v > -inf): "x > below(v)" is "x >= v".
+__device__ __forceinline__ float below(float v) {
+  if (v == 0.f) return __uint_as_float(0x80000001u);
+  return from_ordered(ordered(v) - 1);
+}
+// Sorts by value, then by lower index.
+__device__ __forceinline__ uint64_t make_key(float v, int index) {
+  return (uint64_t(ordered(v)) << 32) | uint32_t(~index);
+}
+__device__ __forceinline__ float key_value(uint64_t key) { return from_ordered(uint32_t(key >> 32)); }
+__device__ __forceinline__ int key_index(uint64_t key) { return int(~uint32_t(key)); }
+
+// Running softmax statistics of part of a row; empty: s = 0.
+struct Stat {
+  float m, s, t;
+};
+// Joins b into a; c2 = scale log2 e.
+__device__ __forceinline__ void join(Stat &a, const Stat &b, float c2) {
+  const float m = fmaxf(a.m, b.m);
+  const float da = (a.m - m) * c2, db = (b.m - m) * c2;
+  const float fa = exp2f(da), fb = exp2f(db);
+  // a part scaled to nothing adds nothing (its t would be 0 * infinity)
+  const float ta = fa > 0.f ? fa * (a.t + da * a.s) : 0.f;
+  const float tb = fb > 0.f ? fb * (b.t + db * b.s) : 0.f;
+  a = Stat{m, fa * a.s + fb * b.s, ta + tb};
+}
+
+// Cuts the list of n keys to its k best, exactly (k < n <= kListCap), and
+// returns the smallest kept value.  Two searches by counting: the k-th
+// largest value bit by bit, then, if more than k reach it, the highest index
+// to keep among those equal to it.  One wave; the list is in its LDS.
+__device__ __forceinline__ float cut_list(uint64_t *list, int n, int k) {
+  constexpr int kPer = kListCap / 64;   // 9
+  const int lane = threadIdx.x & 63;
+  uint64_t e[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) e[i] = lane + 64 * i < n ? list[lane + 64 * i] : 0;
+  const int used = (n + 63) / 64;
+  auto count_at_least = [&](uint64_t key) {
+    int c = 0;
+    for (int i = 0; i < kPer; ++i)
+      if (i < used) c += __popcll(__ballot(e[i] >= key));
+    return c;
+  };
+  // the largest key that k entries reach (keys are distinct, so exactly k)
+  uint64_t key = 0;
+  for (int bit = 63; bit >= 0; --bit) {
+    const uint64_t probe = key | (uint64_t(1) << bit);
+    const int c = count_at_least(probe);
+    if (c >= k) key = probe;
+    if (c == k) break;
+  }
+  int at = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const bool keep = e[i] >= key && e[i] != 0;
+    const uint64_t mask = __ballot(keep);
+    if (keep) list[at + __popcll(mask & ((uint64_t(1) << lane) - 1))] = e[i];
+    at += __popcll(mask);
+  }
+  // the k kept keys now lie in the first k places; their smallest value
+  uint64_t least = ~uint64_t(0);
+  __builtin_amdgcn_wave_barrier();
+  if (lane < k) least = list[lane];
+  uint32_t hi = uint32_t(least >> 32);
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) hi = min(hi, uint32_t(__shfl_xor(int(hi), m)));
+  return from_ordered(hi);
+}
+
+// First tile: a value that at least k of the wave's elements reach, the k-th
+// largest of its 256 chunk maxima or a little below (-inf if fewer are above).
+__device__ __forceinline__ float first_threshold(const float cmax[kUnroll], int k) {
+  uint32_t o[kUnroll];
+#pragma unroll
+  for (int c = 0; c < kUnroll; ++c) o[c] = ordered(cmax[c]);
+  uint32_t v = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t probe = v | (1u << bit);
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < kUnroll; ++c) n += __popcll(__ballot(o[c] >= probe));
+    if (n >= k) v = probe;
+    if (n >= k && n <= k + k / 8) break;
+  }
+  const float f = from_ordered(v);
+  return f > -INFINITY ? f : -INFINITY;    // also for patterns below -inf
+}
+
+// scale (l - m); halves, so that the difference of two large floats stays
+// finite where its product with the scale is.
+__device__ __forceinline__ float scaled_difference(float l, float m, float scale) {
+  return (0.5f * l - 0.5f * m) * scale * 2.f;
+}
+
+// The final outputs of a row from its joined statistics.
+struct RowOut {
+  float m, log_s, entropy, logprob;
+  int rank;
+  bool bad, empty;
+};
+__device__ __forceinline__ RowOut finish_row(const ScoreArgs &a, const Stat &st, int rank_count,
+                                             int64_t id, float given) {
+  RowOut o;
+  const float nan = __uint_as_float(0x7fc00000u);
+  o.bad = !(st.s >= 0.f) || st.m == INFINITY;     // NaN or +inf somewhere
+  o.empty = st.s == 0.f;
+  o.m = st.m;
+  o.log_s = logf(st.s);
+  o.entropy = o.bad ? nan : o.empty ? 0.f : o.log_s - 0.6931471805599453f * (st.t / st.s);
+  o.rank = rank_count;
+  o.logprob = o.empty ? -INFINITY : scaled_difference(given, o.m, a.scale) - o.log_s;
+  if (o.bad) o.logprob = nan, o.rank = -1;
+  if (id >= a.vocab) o.logprob = nan, o.rank = -1;
+  if (id < 0) o.logprob = o.bad ? nan : 0.f, o.rank = -1;
+  return o;
+}
+__device__ __forceinline__ void write_scalars(const ScoreArgs &a, int64_t row, const RowOut &o) {
+  if (a.ids) {
+    if (a.logprob) a.logprob[row] = o.logprob;
+    if (a.rank) a.rank[row] = o.rank;
+  }
+  if (a.entropy) a.entropy[row] = o.entropy;
+}
+// Place p of the row's alternatives.
+__device__ __forceinline__ void write_top(const ScoreArgs &a, int64_t row, int p, const RowOut &o,
+                                          bool present, uint64_t key) {
+  const float nan = __uint_as_float(0x7fc00000u);
+  a.top_ids[row * a.k + p] = o.bad || !present ? -1 : key_index(key);
+  a.top_logprobs[row * a.k + p] =
+      o.bad ? nan : present ? scaled_difference(key_value(key), o.m, a.scale) - o.log_s : -INFINITY;
+}
+
+__device__ __forceinline__ float load_one(const float *p) { return *p; }
+__device__ __forceinline__ float load_one(const bf16_t *p) { return widen(*p); }
+__device__ __forceinline__ float load_one(const f16_t *p) { return widen(*p); }
+
+// Workgroup (row, split): the row's elements [split seg, split seg + seg).
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
+  __shared__ uint64_t lists[TOP ? kWaves * kListCap : 1];
+  __shared__ Stat slot[kWaves];
+  __shared__ int slot_rank[kWaves], slot_n[kWaves];
+  const int64_t row = blockIdx.x / a.splits;
+  const int split = blockIdx.x % a.splits;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const T *l = static_cast<const T *>(a.logits) + row * a.ld;
+  const int v0 = split * a.seg, v1 = min(v0 + a.seg, a.vocab);
+  const float c2 = a.scale * 1.4426950408889634f;
+
+  const int64_t id = a.ids ? a.ids[row] : -1;
+  const bool given = id >= 0 && id < a.vocab;
+  const int at = given ? int(id) : 0;
+  const float lt = given ? load_one(l + at) : 0.f;
+  const float lt_below = lt > -INFINITY ? below(lt) : INFINITY;
+
+  Stat st{-3.402823466e38f, 0.f, 0.f};
+  int ahead = 0;
+  uint64_t *list = lists + (TOP ? wave * kListCap : 0);
+  int n = 0;                       // list length (wave-uniform)
+  float thr = -INFINITY;           // candidates are > thr
+  const int limit = 2 * a.k + 32;  // list length that is cut after a tile
+
+  for (int tile = v0; tile < v1; tile += kUnroll * kChunkElems) {
+    float x[kUnroll][8], cmax[kUnroll];
+#pragma unroll
+    for (int c = 0; c < kUnroll; ++c) {
+      const int e0 = tile + c * kChunkElems + 8 * tid, left = v1 - e0;
+      load8(l + min(e0, a.vocab - 1), left, x[c]);
+      if (left < 8) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j >= left) x[c][j] = -INFINITY;
+      }
+    }
+    float m = st.m;
+#pragma unroll
+    for (int c = 0; c < kUnroll; ++c) {
+      cmax[c] = x[c][0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) cmax[c] = fmaxf(cmax[c], x[c][j]);
+      m = fmaxf(m, cmax[c]);
+    }
+    if (m > st.m) {                // rescale to the new maximum
+      const float dm = (st.m - m) * c2, f = __builtin_amdgcn_exp2f(dm);
+      st.t = f > 0.f ? f * (st.t + dm * st.s) : 0.f;
+      st.s *= f;
+      st.m = m;
+    }
+#pragma unroll
+    for (int c = 0; c < kUnroll; ++c)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = (x[c][j] - m) * c2;
+        const float e = __builtin_amdgcn_exp2f(d);
+        st.s += e;
+        st.t += fmaxf(d, -3e38f) * e;   // -inf: 0
+      }
+    if (given) {
+#pragma unroll
+      for (int c = 0; c < kUnroll; ++c) {
+        // Entries before the given token count from its value up, entries
+        // after it from above its value.
+        const int e0 = tile + c * kChunkElems + 8 * tid;
+        const bool before = e0 + 7 < at;
+        const float from = before ? lt_below : lt;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ahead += x[c][j] > from;
+        if (before && e0 < v1 && lt == -INFINITY) ahead += 8;   // all of them: >= -inf
+        if (!before && e0 < at && e0 < v1) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ahead += (e0 + j < at) && x[c][j] == lt;
+        }
+      }
+    }
+    if (TOP) {
+      float strict = thr;
+      if (tile == v0) {
+        strict = first_threshold(cmax, a.k);
+        if (strict > -INFINITY) thr = below(strict);
+      }
+#pragma unroll
+      for (int c = 0; c < kUnroll; ++c) {
+        if (!__ballot(cmax[c] > thr)) continue;
+        int add = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) add += __popcll(__ballot(x[c][j] > thr));
+        if (n + add > kListCap) {      // wave-uniform; then n is k and a chunk fits
+          strict = cut_list(list, n, a.k);
+          thr = fmaxf(thr, strict);
+          n = a.k;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool take = x[c][j] > thr;
+          const uint64_t mask = __ballot(take);
+          if (take)
+            list[n + __popcll(mask & ((uint64_t(1) << lane) - 1))] =
+                make_key(x[c][j], tile + c * kChunkElems + 8 * tid + j);
+          n += __popcll(mask);
+        }
+      }
+      // Later entries that only equal the threshold have higher indices than
+      // the k entries that reach it.
+      thr = fmaxf(thr, strict);
+      if (n > limit) {
+        thr = fmaxf(thr, cut_list(list, n, a.k));
+        n = a.k;
+      }
+    }
+  }
+
+  // Join the lanes, then the waves, in a fixed order.
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const Stat o{__shfl_xor(st.m, m), __shfl_xor(st.s, m), __shfl_xor(st.t, m)};
+    // same operand order on both sides, so both get the same bits
+    Stat lo = lane & m ? o : st;
+    join(lo, lane & m ? st : o, c2);
+    st = lo;
+  }
+  ahead = wave_all<SumI>(ahead);
+  if (TOP && n > a.k) {
+    cut_list(list, n, a.k);
+    n = a.k;
+  }
+  if (lane == 0) {
+    slot[wave] = st;
+    slot_rank[wave] = ahead;
+    slot_n[wave] = n;
+  }
+  __syncthreads();
+  st = slot[0];
+  ahead = slot_rank[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) {
+    join(st, slot[w], c2);
+    ahead += slot_rank[w];
+  }
+  const bool whole = a.splits == 1;
+  RowOut o;
+  if (whole) {
+    o = finish_row(a, st, ahead, id, lt);
+    if (tid == 0) write_scalars(a, row, o);
+  } else if (tid == 0) {
+    float *p = a.part + int64_t(blockIdx.x) * kPartWords;
+    p[0] = st.m;
+    p[1] = st.s;
+    p[2] = st.t;
+    p[3] = __int_as_float(ahead);
+  }
+  if (TOP) {
+    // The waves' lists (at most k keys each): a key's place is the number of
+    // larger ones.  Thread w * 64 + i holds entry i of wave w's list.
+    const bool mine = lane < slot_n[wave];
+    const uint64_t key = mine ? list[lane] : 0;
+    int place = 0, total = 0;
+    for (int w = 0; w < kWaves; ++w) {
+      const int nw = slot_n[w];
+      total += nw;
+      for (int i = 0; i < nw; ++i) place += lists[w * kListCap + i] > key;
+    }
+    if (whole) {
+      if (mine && place < a.k) write_top(a, row, place, o, true, key);
+      if (tid >= total && tid < a.k) write_top(a, row, tid, o, false, 0);
+    } else {
+      uint64_t *out = a.part_keys + int64_t(blockIdx.x) * a.k;
+      if (mine && place < a.k) out[place] = key;
+      if (tid >= total && tid < a.k) out[tid] = 0;    // no key is 0
+    }
+  }
+}
+
+// Joins a row's splits: one workgroup per row.  More keys than kDirect are
+// first cut to the k best by the same search as a wave's list (the largest
+// key that k entries reach), over the workgroup.
+constexpr int kDirect = 256;
+constexpr int kMaxSplits = 64;
+template <typename T>
+__global__ void __launch_bounds__(kThreads) score_join_kernel(ScoreArgs a) {
+  __shared__ uint64_t keys[kDirect];
+  __shared__ int counts[2][kWaves], kept;
+  constexpr int kPer = kMaxSplits * kMaxTop / kThreads;   // 16
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const float c2 = a.scale * 1.4426950408889634f;
+  const int64_t id = a.ids ? a.ids[row] : -1;
+  const bool given = id >= 0 && id < a.vocab;
+  const float lt = given ? load_one(static_cast<const T *>(a.logits) + row * a.ld + id) : 0.f;
+  const float *p = a.part + row * a.splits * kPartWords;
+  Stat st{p[0], p[1], p[2]};
+  int ahead = __float_as_int(p[3]);
+  for (int s = 1; s < a.splits; ++s) {
+    const float *q = p + s * kPartWords;
+    join(st, Stat{q[0], q[1], q[2]}, c2);
+    ahead += __float_as_int(q[3]);
+  }
+  const RowOut o = finish_row(a, st, ahead, id, lt);
+  if (tid == 0) write_scalars(a, row, o);
+  if (a.k == 0) return;
+  int n = a.splits * a.k;
+  const uint64_t *src = a.part_keys + row * n;
+  if (n <= kDirect) {
+    keys[tid] = tid < n ? src[tid] : 0;
+  } else {
+    uint64_t e[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) e[i] = tid + kThreads * i < n ? src[tid + kThreads * i] : 0;
+    if (tid == 0) kept = 0;
+    uint64_t key = 0;
+    for (int bit = 63; bit >= 0; --bit) {
+      const uint64_t probe = key | (uint64_t(1) << bit);
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (kThreads * i < n) c += __popcll(__ballot(e[i] >= probe));
+      if ((tid & 63) == 0) counts[bit & 1][wave] = c;
+      __syncthreads();
+      c = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) c += counts[bit & 1][w];
+      if (c >= a.k) key = probe;
+      if (c == a.k) break;
+    }
+    keys[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (e[i] != 0 && e[i] >= key)      // at most k of them, in any order
+        keys[atomicAdd(&kept, 1)] = e[i];
+    n = a.k;
+  }
+  __syncthreads();
+  const uint64_t key = tid < n ? keys[tid] : 0;
+  int place = 0, total = 0;
+  for (int i = 0; i < n; ++i) {
+    place += keys[i] > key;
+    total += keys[i] != 0;
+  }
+  if (key != 0 && place < a.k) write_top(a, row, place, o, true, key);
+  if (tid >= total && tid < a.k) write_top(a, row, tid, o, false, 0);
+}
+
+// A row is split over workgroups until the launch has about four of them
+// per compute unit; a split takes whole chunks.
+struct ScorePlan {
+  int splits, seg;
+};
+ScorePlan score_plan(int64_t rows, int64_t vocab, int cus) {
+  const int64_t chunks = cdiv(vocab, kChunkElems);
+  const int64_t want = std::min<int64_t>(chunks, cdiv(4 * int64_t(cus), rows));
+  const int64_t per = cdiv(chunks, std::min<int64_t>(want, kMaxSplits));
+  return {int(cdiv(chunks, per)), int(per * kChunkElems)};
+}
+
+constexpr size_t kPartBytes = kPartWords * sizeof(float);
+
+size_t score_ws(int64_t rows, int64_t vocab, int32_t k, int cus) {
+  const ScorePlan p = score_plan(rows, vocab, cus);
+  if (p.splits == 1) return 0;
+  return align256(size_t(rows) * p.splits * kPartBytes) +
+         align256(size_t(rows) * p.splits * size_t(k) * sizeof(uint64_t));
+}
+
+template <typename T>
+gptq_status score_typed(const ScoreArgs &a, int64_t rows, hipStream_t s) {
+  const dim3 grid(uint32_t(rows * a.splits));
+  GPTQ_TRY(a.k ? launch("token_logprobs", score_kernel<T, true>, grid, dim3(kThreads), 0, s, a)
+               : launch("token_logprobs", score_kernel<T, false>, grid, dim3(kThreads), 0, s, a));
+  if (a.splits == 1) return GPTQ_OK;
+  return launch("token_logprobs_join", score_join_kernel<T>, dim3(uint32_t(rows)), dim3(kThreads), 0,
+                s, a);
+}
+
+constexpr int64_t kMaxVocab = int64_t(1) << 24, kMaxScoreRows = int64_t(1) << 24;
+bool valid_score(int64_t rows, int64_t vocab, int32_t k) {
+  return rows >= 0 && rows <= kMaxScoreRows && vocab >= 1 && vocab <= kMaxVocab && k >= 0 &&
+         k <= kMaxTop && k <= vocab;
+}
+
+}  // namespace
+}  // namespace gptq
+
+using namespace gptq;
+
+extern "C" {
+
+size_t gptq_token_logprobs_ws_bytes(int64_t rows, int64_t vocab, int32_t top_k) {
+  if (!valid_score(rows, vocab, top_k) || rows == 0) return 0;
+  return score_ws(rows, vocab, top_k, device_cu_count());
+}
+
+gptq_status gptq_token_logprobs(const void *logits, int32_t dtype, int64_t rows, int64_t vocab,
+                                int64_t ld, const int64_t *ids, float scale, int32_t top_k,
+                                float *logprob, int32_t *rank, float *entropy, int32_t *top_ids,
+                                float *top_logprobs, void *ws, size_t ws_bytes, void *stream) {
+  return guarded([&]() -> gptq_status {
+    if (!valid_score(rows, vocab, top_k))
+      return fail(GPTQ_ERR_INVALID_ARG,
+                  "rows and vocab must be in [0, 2^24] x [1, 2^24], top_k in [0, min(64, vocab)]");
+    if (!is_float_type(dtype))
+      return fail(GPTQ_ERR_INVALID_ARG, "the logits' type must be F32, BF16 or F16");
+    if (!(scale > 0.f) || !(scale < HUGE_VALF))
+      return fail(GPTQ_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (rows == 0) return GPTQ_OK;
+    if (!logits) return fail(GPTQ_ERR_INVALID_ARG, "logits must not be NULL");
+    if (!aligned_to(logits, type_bytes(dtype)) || !aligned_to(ids, 8))
+      return fail(GPTQ_ERR_INVALID_ARG, "logits and ids must be aligned to their elements");
+    if (ld < vocab) return fail(GPTQ_ERR_INVALID_ARG, "ld must be >= vocab");
+    if (top_k > 0 && (!top_ids || !top_logprobs))
+      return fail(GPTQ_ERR_INVALID_ARG, "top_ids and top_logprobs must not be NULL");
+    if ((logprob || rank) && !ids)
+      return fail(GPTQ_ERR_INVALID_ARG, "logprob and rank need ids");
+    for (const void *p : {(const void *)logprob, (const void *)rank, (const void *)entropy,
+                          (const void *)top_ids, (const void *)top_logprobs})
+      if (!aligned_to(p, 4)) return fail(GPTQ_ERR_INVALID_ARG, "outputs must be 4-byte aligned");
+    const int cus = device_cu_count();
+    const ScorePlan plan = score_plan(rows, vocab, cus);
+    const size_t need = score_ws(rows, vocab, top_k, cus);
+    if (need) {
+      if (!ws) return fail(GPTQ_ERR_WORKSPACE, "workspace is NULL");
+      if (!aligned_to(ws, 256))
+        return fail(GPTQ_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+      if (ws_bytes < need)
+        return fail(GPTQ_ERR_WORKSPACE, "workspace too small: need " + std::to_string(need) +
+                                            " bytes, got " + std::to_string(ws_bytes));
+    }
+    ScoreArgs a;
+    a.logits = logits;
+    a.ids = ids;
+    a.ld = ld;
+    a.vocab = int(vocab);
+    a.k = top_k;
+    a.splits = plan.splits;
+    a.seg = plan.seg;
+    a.scale = scale;
+    a.logprob = logprob;
+    a.rank = rank;
+    a.entropy = entropy;
+    a.top_ids = top_ids;
+    a.top_logprobs = top_logprobs;
+    a.part = static_cast<float *>(ws);
+    a.part_keys = reinterpret_cast<uint64_t *>(
+        static_cast<char *>(ws) + (need ? align256(size_t(rows) * plan.splits * kPartBytes) : 0));
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    if (dtype == GPTQ_DT_F32) return score_typed<float>(a, rows, s);
+    if (dtype == GPTQ_DT_BF16) return score_typed<bf16_t>(a, rows, s);
+    return score_typed<f16_t>(a, rows, s);
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,576 @@
+"""The operators that run and score a per-row 8-bit layer, on the GPU through
+the C ABI, against their float64 definitions.
+
+Codes, sums of codes, ranks and token ids are compared exactly, and so is the
+product (one rounding of an exact integer, one of a float32 product, one to
+the output type).  The floats of the norm block, of silu(g) u and of the
+scoring are held to bounds on their float32 arithmetic, derived beside them."""
+import numpy as np
+import pytest
+
+from oracle import run_oracle as R
+from tests.gpu_harness import log
+
+pytestmark = pytest.mark.gpu
+
+U32 = 2.0 ** -24
+ULP = {"f32": 2.0 ** -24, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}   # unit roundoff
+TINY = {"f32": 2.0 ** -126, "f16": 2.0 ** -24, "bf16": 2.0 ** -126}
+
+
+def torch_type(kind):
+    import torch
+    return {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[kind]
+
+
+def to_gpu(x, kind="f32"):
+    """float64 / float32 values rounded to the type, as a device tensor."""
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(x, np.float32)).cuda().to(torch_type(kind))
+
+
+def back(t):
+    """Device tensor -> the float32 it stands for (every type here widens exactly)."""
+    return t.float().cpu().numpy()
+
+
+def placed(x, how):
+    """The same matrix with other strides and alignment: rows cut out of wider ones."""
+    import torch
+    if how == "plain":
+        return x
+    wide = torch.full((x.shape[0], x.shape[1] + 5), 7.0, dtype=x.dtype, device=x.device)
+    lo = {"left": 0, "odd": 1}[how]
+    wide[:, lo:lo + x.shape[1]] = x
+    return wide[:, lo:lo + x.shape[1]]
+
+
+# ------------------------------------------------------------- token codes
+
+def activations(rng, t, cols):
+    x = rng.standard_normal((t, cols)) * np.exp(rng.standard_normal((t, 1)))
+    x[:, rng.random(cols) < 0.05] *= 20
+    return x
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("t,cols,how", [
+    (1, 1, "plain"), (3, 7, "odd"), (5, 128, "plain"), (4, 129, "left"), (2, 1001, "odd"),
+    (3, 4100, "plain"), (2, 11008, "plain"), (1, 33000, "odd"), (2, 65536, "plain"),
+    (1030, 96, "plain"), (1029, 1500, "odd"), (1025, 2500, "plain"), (1024, 9000, "left")])
+def test_quantize_tokens(kind, t, cols, how):
+    from post_weight_quantization_layer_amd.w8a8 import TokenCodes, quantize_tokens
+    rng = np.random.default_rng(t * 7 + cols)
+    x = placed(to_gpu(activations(rng, t, cols), kind), how)
+    out = TokenCodes(t, cols)
+    out.codes.fill_(99)
+    quantize_tokens(x, out)
+    q, s, n = R.token_codes(back(x))
+    codes = out.codes.cpu().numpy()
+    np.testing.assert_array_equal(codes[:, :cols], q)
+    assert not codes[:, cols:].any()          # the pad
+    np.testing.assert_array_equal(out.scale.cpu().numpy(), s)
+    np.testing.assert_array_equal(out.sum.cpu().numpy(), n)
+
+
+def test_quantize_tokens_special_rows():
+    from post_weight_quantization_layer_amd.w8a8 import quantize_tokens
+    x = np.zeros((9, 300), np.float32)
+    x[1, 5] = np.nan
+    x[2, 299] = np.inf
+    x[3, 7] = -np.inf
+    x[4, :4] = [1e-45, -1e-45, 0, 0]                  # scale underflows to 0
+    x[5, :4] = [190e-45, -3e-45, 7e-45, 0]            # scale is subnormal
+    x[6, :3] = [3.4028235e38, -3.4028235e38, 1e38]    # largest floats
+    x[7] = 5.0
+    x[8, :3] = [1e-30, -2e-30, 3e-31]
+    out = quantize_tokens(to_gpu(x))
+    q, s, n = R.token_codes(x)
+    np.testing.assert_array_equal(out.scale.cpu().numpy(), s)
+    np.testing.assert_array_equal(out.codes.cpu().numpy()[:, :300], q)
+    np.testing.assert_array_equal(out.sum.cpu().numpy(), n)
+
+
+def test_quantize_tokens_ties():
+    """Values placed on and beside half steps: the correctly rounded quotient decides."""
+    from post_weight_quantization_layer_amd.w8a8 import quantize_tokens
+    for scale in (1.0, 1.0 / 3, 0.0123456789):
+        half = (np.arange(-126, 126) + 0.5) * scale
+        x = np.stack([half, np.nextafter(half.astype(np.float32), np.float32(9)),
+                      np.nextafter(half.astype(np.float32), np.float32(-9))]).astype(np.float32)
+        x = np.concatenate([x, np.full((3, 1), 127 * scale, np.float32)], axis=1)
+        out = quantize_tokens(to_gpu(x))
+        np.testing.assert_array_equal(out.codes.cpu().numpy()[:, :x.shape[1]],
+                                      R.token_codes(x)[0])
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("t,cols", [(1, 1), (3, 130), (2, 11008), (1, 40000), (1024, 700),
+                                    (5, 4099)])
+def test_silu_mul_quantize(kind, t, cols):
+    """silu(g) u in float32: exp is within 2 ulp (4 u), the sum 1 + e adds u, the
+    quotient and the product u each: 8 u with the second-order rest.  So the
+    scale is within 9 u of the exact one, a value over the scale within 18 u,
+    at most 127 * 18 u < 1.4e-4 steps from the exact one, and its code within
+    0.5 + 1.4e-4 of that."""
+    from post_weight_quantization_layer_amd.w8a8 import silu_mul_quantize
+    rng = np.random.default_rng(cols)
+    gu = to_gpu(3 * rng.standard_normal((t, 2 * cols)), kind)
+    out = silu_mul_quantize(gu[:, :cols], gu[:, cols:])
+    f = back(gu).astype(np.float64)
+    a = R.silu_mul(f[:, :cols], f[:, cols:])
+    s = np.abs(a).max(axis=1) / 127
+    np.testing.assert_allclose(out.scale.cpu().numpy(), s, rtol=9 * U32)
+    codes = out.codes.cpu().numpy()
+    assert np.abs(codes[:, :cols] - a / s[:, None]).max() <= 0.5 + 1.4e-4
+    assert not codes[:, cols:].any()
+    np.testing.assert_array_equal(out.sum.cpu().numpy(), codes.astype(np.int64).sum(axis=1))
+
+
+# ----------------------------------------------------------------- product
+
+def stored_layer(rng, rows, cols):
+    codes = np.clip(np.rint(rng.standard_normal((rows, cols)) * 32 + 128), 0, 255).astype(np.uint8)
+    scale = np.exp(rng.standard_normal(rows) * 0.3).astype(np.float32) * 1e-3
+    return codes, scale, rng.integers(100, 156, rows).astype(np.uint8)
+
+
+def layer_on_gpu(codes, scale, zero):
+    import torch
+    from post_weight_quantization_layer_amd.w8a8 import W8A8Linear
+    return W8A8Linear(torch.from_numpy(codes).cuda(), torch.from_numpy(scale).cuda(),
+                      torch.from_numpy(zero).cuda())
+
+
+def expected_product(q, s, codes, scale, zero, kind):
+    import torch
+    sums = R.product_sums(q, codes, zero).astype(np.int32).astype(np.float32)
+    y = sums * (s[:, None] * scale[None, :])
+    assert y.dtype == np.float32
+    return back(torch.from_numpy(y).to(torch_type(kind)))
+
+
+SIZES = [(1, 1, 1), (1, 16, 128), (2, 17, 130), (3, 15, 127), (5, 300, 1000), (15, 64, 64),
+         (16, 100, 256), (17, 513, 384), (31, 48, 4100), (33, 1000, 129), (64, 257, 512),
+         (65, 256, 640), (100, 33, 11008), (130, 130, 130), (257, 520, 300), (300, 1031, 200),
+         (515, 768, 1152), (1, 4096, 11008), (4, 5000, 2048), (8, 4096, 4096), (16, 9000, 640),
+         (700, 2100, 260), (1, 70, 65536), (1030, 520, 136)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("t,rows,cols", SIZES)
+def test_product_is_exact(kind, t, rows, cols):
+    import torch
+    rng = np.random.default_rng(t + 3 * rows + 5 * cols)
+    codes, scale, zero = stored_layer(rng, rows, cols)
+    lin = layer_on_gpu(codes, scale, zero)
+    x = to_gpu(activations(rng, t, cols), kind)
+    q, s, n = R.token_codes(back(x))
+    want = expected_product(q, s, codes, scale, zero, kind)
+    got = lin(x)
+    np.testing.assert_array_equal(back(got), want)
+    # the two-call form, into a strided output whose other columns stay as they are
+    from post_weight_quantization_layer_amd.w8a8 import quantize_tokens
+    wide = torch.full((t, rows + 3), 5.0, dtype=x.dtype, device="cuda")
+    lin.product(quantize_tokens(x), wide[:, 1:rows + 1])
+    np.testing.assert_array_equal(back(wide[:, 1:rows + 1]), want)
+    assert (wide[:, 0] == 5).all() and (wide[:, rows + 1:] == 5).all()
+
+
+@pytest.mark.parametrize("t", [1, 7, 40, 300])
+@pytest.mark.parametrize("code,zero", [(255, 0), (0, 255), (255, 255), (0, 0)])
+def test_product_extremes_fit(t, code, zero):
+    """Every code at its end and the widest layer: sums up to 127 * 255 * 65536."""
+    import torch
+    rows, cols = 33, 65536
+    lin = layer_on_gpu(np.full((rows, cols), code, np.uint8), np.ones(rows, np.float32),
+                       np.full(rows, zero, np.uint8))
+    x = torch.full((t, cols), -127.0, device="cuda")
+    x[0] = 127.0
+    y = lin(x)
+    want = np.float32(127 * (code - zero) * cols)
+    got = back(y)
+    assert (got[0] == want).all() and (got[1:] == -want).all()
+
+
+def test_product_other_types_strides_and_bad_rows():
+    import torch
+    rng = np.random.default_rng(11)
+    codes, scale, zero = stored_layer(rng, 70, 200)
+    lin = layer_on_gpu(codes, scale, zero)
+    x = activations(rng, 20, 200).astype(np.float32)
+    x[3, 0], x[4, 1], x[5] = np.nan, np.inf, 0
+    xg = placed(to_gpu(x, "f32"), "odd")
+    y = torch.empty((20, 70), dtype=torch.bfloat16, device="cuda")
+    lin(xg, y)
+    got = back(y)
+    q, s, n = R.token_codes(x)
+    want = expected_product(q, s, codes, scale, zero, "bf16")
+    np.testing.assert_array_equal(got, want)
+    assert np.isnan(got[3]).all() and np.isnan(got[4]).all() and (got[5] == 0).all()
+    assert lin(xg[:0]).shape == (0, 70)
+
+
+def test_product_of_quantized_layers_stacked():
+    """Layers from the quantizer, stacked: the product is x W^ of the dequantized weights."""
+    import torch
+    from post_weight_quantization_layer_amd.layer import GptqLayer
+    from post_weight_quantization_layer_amd.w8a8 import W8A8Linear
+    rng = np.random.default_rng(5)
+    d, rows, n = 256, 48, 512
+    X = to_gpu(rng.standard_normal((d, n)), "bf16")
+    L = GptqLayer(rows, d, bits=8, group=d, block=128, act_order=True)
+    L.reset_hessian()
+    L.add_batch(X)
+    L.prepare()
+    qs = [L.quantize(to_gpu(rng.standard_normal((rows, d)) * 0.02)) for _ in range(2)]
+    lin = W8A8Linear.from_quantized(*qs)
+    x = to_gpu(rng.standard_normal((9, d)), "f16")
+    q, s, _ = R.token_codes(back(x))
+    w = np.concatenate([back(q.W_hat) for q in qs]).astype(np.float64)
+    want = (q * s[:, None].astype(np.float64)) @ w.T
+    # W^ = scale (c - z) is rounded to float32 once per weight, y once more and to float16
+    mag = np.abs(q * s[:, None].astype(np.float64)) @ np.abs(w).T
+    err = np.abs(back(lin(x)) - want)
+    assert (err <= 2.0 ** -11 * np.abs(want) + 4 * U32 * mag + 2.0 ** -25).all()
+    with pytest.raises(ValueError):
+        G = GptqLayer(rows, d, bits=8, group=128, block=128, act_order=False)
+        G.H, G.hdiag = L.H, L.hdiag
+        G.prepare()
+        W8A8Linear.from_quantized(G.quantize(to_gpu(rng.standard_normal((rows, d)))))
+
+
+# --------------------------------------------------------------- norm block
+
+# Longest chain of float32 additions into a row's sum: 32 values of a lane
+# (their squares rounded too), 6 + 16 joins over lanes and waves; then the
+# division, eps, root, reciprocal and the products.
+CHAIN = 32 + 32 + 6 + 16 + 10
+
+
+def norm_bound(v, dv, kind, w, bias, eps, off):
+    """Float64 norm of v and a bound on its float32 error, given v's bound dv."""
+    y = R.norm(v, kind, w, bias, eps, off)
+    if kind in (None, "none"):
+        return y, dv
+    n = v.shape[1]
+    mean = v.mean(axis=1, keepdims=True) if kind == "layer" else 0.0
+    # the mean's own error, and v - mean's
+    dc = dv + (dv.mean(axis=1, keepdims=True)
+               + CHAIN * U32 * np.abs(v).mean(axis=1, keepdims=True) + U32 * np.abs(v)
+               if kind == "layer" else 0.0)
+    c = v - mean
+    ms = (c * c).mean(axis=1, keepdims=True) + eps
+    rstd = 1 / np.sqrt(ms)
+    # relative error of rstd: half that of the mean square
+    rel = (np.sqrt((dc * dc).mean(axis=1, keepdims=True)) * np.sqrt((c * c).mean(axis=1, keepdims=True))
+           + (dc * dc).mean(axis=1, keepdims=True)) / ms + CHAIN * U32
+    gain = np.ones(n) if w is None else np.abs(off + np.asarray(w, np.float64))
+    scaled = np.abs(c) * rstd * gain
+    return y, dc * rstd * gain * (1 + rel) + scaled * (rel + 8 * U32) + \
+        U32 * (0 if bias is None else np.abs(bias)) * 2
+
+
+def check_close(got, want, bound, kind, what):
+    tol = bound * 1.01 + ULP[kind] * (np.abs(want) + bound) + TINY[kind]
+    err = np.abs(got - want)
+    worst = float((err / tol).max())
+    log(f"norm_block {what} {kind}: worst error {worst:.3f} of its bound")
+    assert worst <= 1, what
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("t,d,post,pre,gates,w_kind,how", [
+    (1, 1, "rms", "rms", None, None, "plain"), (1, 4096, "rms", "rms", None, "f32", "plain"),
+    (3, 7, "layer", "layer", "token", "same", "odd"), (5, 513, "rms", "layer", "all", "bf16", "left"),
+    (2, 8192, "layer", "rms", "pairs", "f16", "plain"), (4, 1001, None, "rms", "token", "same", "odd"),
+    (2, 16384, "rms", None, "all", "f32", "plain"), (1, 32768, "layer", "layer", "token", "same", "plain"),
+    (1030, 64, "rms", "rms", "pairs", "same", "plain"), (1024, 515, "layer", "layer", "token", "f32", "odd"),
+    (1027, 2000, "rms", "layer", "all", "same", "plain"), (1025, 5000, "layer", "rms", None, "same", "left"),
+    (1024, 12288, "rms", "rms", "pairs", "f16", "plain")])
+def test_norm_block(kind, t, d, post, pre, gates, w_kind, how):
+    import torch
+    from post_weight_quantization_layer_amd.norms import NormBlock
+    rng = np.random.default_rng(d + t)
+    w_kind = kind if w_kind == "same" else w_kind
+    r = placed(to_gpu(3 * activations(rng, t, d), kind), how)
+    b = placed(to_gpu(activations(rng, t, d) + 0.5, kind), how)
+    vec = [to_gpu(m + 0.3 * rng.standard_normal(d), w_kind) if w_kind else None
+           for m in (1.0, 0.0, 0.2, 0.0)]
+    each = {None: 1, "all": t, "pairs": 2, "token": 1}[gates]
+    gate = to_gpu(rng.standard_normal((-(-t // each), d)), kind) if gates else None
+    off = 1.0 if d % 2 else 0.0
+    op = NormBlock(d, post=post, post_weight=vec[0], post_bias=vec[1], pre=pre, pre_weight=vec[2],
+                   pre_bias=vec[3], residual_scale=0.75, block_scale=1.5, eps=1e-5,
+                   weight_offset=off)
+    r_out, h = op(r, b, gate=gate, gate_tokens=each)
+    f = [None if v is None else back(v).astype(np.float64) for v in vec]
+    eps = float(np.float32(1e-5))
+    p, dp = norm_bound(back(b).astype(np.float64), np.zeros((t, d)), post, f[0], f[1], eps, off)
+    if gate is not None:
+        rows = np.repeat(back(gate).astype(np.float64), each, axis=0)[:t]
+        p, dp = p * rows, (dp + U32 * np.abs(p)) * np.abs(rows)
+    R64 = 0.75 * back(r).astype(np.float64)
+    want = R64 + 1.5 * p
+    dr = 1.5 * dp + 2 * U32 * (np.abs(R64) + 1.5 * np.abs(p))
+    check_close(back(r_out), want, dr, kind, "r'")
+    want_h, dh = norm_bound(want, dr, pre, f[2], f[3], eps, off)
+    check_close(back(h), want_h, dh, kind, "h")
+    np.testing.assert_allclose(want_h, R.norm_block(
+        back(r), back(b), rows if gate is not None else None, post=post, post_weight=f[0],
+        post_bias=f[1], pre=pre, pre_weight=f[2], pre_bias=f[3], residual_scale=0.75,
+        block_scale=1.5, eps=eps, weight_offset=off)[1], rtol=1e-9, atol=1e-12)
+
+
+@pytest.mark.parametrize("t,d", [(1, 4096), (3, 130), (1024, 1000), (6, 8200)])
+def test_norm_block_in_place_codes_and_first(t, d):
+    """In place equals out of place; codes are those of the float32 h; no block output."""
+    import torch
+    from post_weight_quantization_layer_amd.norms import NormBlock
+    from post_weight_quantization_layer_amd.w8a8 import TokenCodes, quantize_tokens
+    rng = np.random.default_rng(d)
+    r = to_gpu(activations(rng, t, d))
+    b = to_gpu(activations(rng, t, d))
+    w = to_gpu(1 + 0.1 * rng.standard_normal(d))
+    op = NormBlock(d, post="rms", post_weight=w, pre="layer", pre_weight=w, eps=1e-5)
+    codes = TokenCodes(t, d)
+    codes.codes.fill_(99)
+    h = torch.empty_like(r)
+    want_r, want_h = op(r, b)
+    r_out, got_h = op(r, b, h=h, codes=codes)
+    assert torch.equal(r_out, want_r) and torch.equal(got_h, want_h) and got_h is h
+    # the stream is float32, so h is stored unrounded and its codes must be these
+    ref = quantize_tokens(want_h)
+    assert torch.equal(codes.codes, ref.codes) and torch.equal(codes.scale, ref.scale)
+    assert torch.equal(codes.sum, ref.sum)
+    first = NormBlock(d, pre="layer", pre_weight=w, residual_scale=2.0, eps=1e-5)
+    got = first(r, codes=TokenCodes(t, d))
+    assert got[0] is r
+    scaled = first(r)[1]
+    plain = NormBlock(d, pre="layer", pre_weight=w, eps=1e-5)(r * 2)[1]
+    assert torch.equal(scaled, plain)
+    r2, b2 = r.clone(), b.clone()
+    op(r2, b2, r_out=r2, h=b2)
+    assert torch.equal(r2, want_r) and torch.equal(b2, want_h)
+
+
+def test_norm_block_special_rows():
+    import torch
+    from post_weight_quantization_layer_amd.norms import NormBlock
+    from post_weight_quantization_layer_amd.w8a8 import TokenCodes
+    r = np.ones((5, 40), np.float32)
+    b = np.ones((5, 40), np.float32)
+    r[0] = b[0] = 0
+    r[1, 3] = np.nan
+    b[2, 4] = np.inf
+    r[3], b[3] = 1e-20, -1e-20
+    codes = TokenCodes(5, 40)
+    r_out, h = NormBlock(40, post="rms", pre="rms", eps=1e-6)(
+        to_gpu(r), to_gpu(b), h=torch.empty((5, 40), device="cuda"), codes=codes)
+    h = back(h)
+    assert (h[0] == 0).all() and np.isnan(h[1]).all() and np.isnan(h[2]).any()
+    assert np.isfinite(h[3:]).all()
+    s = codes.scale.cpu().numpy()
+    assert s[0] == 0 and np.isnan(s[1]) and np.isnan(s[2]) and np.isfinite(s[3:]).all()
+
+
+# ------------------------------------------------------------------ scoring
+
+def score_bounds(x, want, scale):
+    """Bounds on logprob (per value z - lse) and entropy.
+
+    d = scale (l - m) is off by 3 u |d|, the power of two by 2 ulp (4 u) of
+    itself; the sum of at most vocab / 256 + 64 terms in a chain adds u each.
+    So s is off by rel = 3 u E|d| + (4 + chain) u with E|d| the mean under p,
+    ln s by as much (and u of itself and 2 u), a log probability by that and
+    3 u of its own d.  t / s = E d is off by its own relative error (2 rel +
+    4 u), plus the second moment's part 3 u E d^2."""
+    vocab = x.shape[1]
+    m = np.where(np.isfinite(x), x, -np.inf).max(axis=1, keepdims=True)
+    d = np.where(np.isfinite(x), scale * (x - np.where(np.isfinite(m), m, 0)), 0)
+    p = np.where(np.isfinite(x), np.exp(d), 0)
+    total = np.maximum(p.sum(axis=1), 1e-300)
+    e1 = (p * np.abs(d)).sum(axis=1) / total
+    e2 = (p * d * d).sum(axis=1) / total
+    chain = vocab / 256 + 64
+    rel = 3 * U32 * e1 + (4 + chain) * U32
+    log_s = rel + U32 * np.abs(np.log(total)) + 2 * U32
+    return log_s, log_s + e1 * (2 * rel + 4 * U32) + 3 * U32 * e2 + U32 * np.abs(want[2])
+
+
+def check_scores(logits, ids, kind, scale, k, how="plain", name=""):
+    import torch
+    from post_weight_quantization_layer_amd.scoring import TokenScorer
+    rows, vocab = logits.shape
+    x = placed(to_gpu(logits, kind), how)
+    with np.errstate(all="ignore"):
+        seen = back(x).astype(np.float64)
+        want = R.token_logprobs(seen, ids, float(np.float32(scale)), k)
+        log_s, ent = score_bounds(seen, want, scale)
+    got = TokenScorer(rows, vocab, k)(x, torch.from_numpy(np.asarray(ids, np.int64)).cuda(),
+                                      scale=scale)
+    np.testing.assert_array_equal(got.rank.cpu().numpy(), want[1])
+    np.testing.assert_array_equal(got.top_ids.cpu().numpy(), want[3])
+
+    def close(a, b, tol):
+        a = a.double().cpu().numpy()
+        with np.errstate(over="ignore"):
+            b = b.astype(np.float32).astype(np.float64)     # past the type: -infinity
+        fin = np.isfinite(b)
+        np.testing.assert_array_equal(np.where(fin, 0, a), np.where(fin, 0, b))
+        err = np.where(fin, np.abs(np.where(fin, a, 0) - np.where(fin, b, 0)), 0)
+        assert ((err <= tol) | ~fin).all(), (name, float(np.nanmax(err / tol)))   # bad rows: no bound
+
+    # a log probability's own difference d, and its last sum
+    own = lambda lp: 6 * U32 * (np.abs(np.where(np.isfinite(lp), lp, 0)) + 2 * np.log(vocab + 1.0))
+    close(got.logprob, want[0], log_s + own(want[0]))
+    close(got.entropy, want[2], ent + 1e-30)
+    close(got.top_logprobs, want[4], log_s[:, None] + own(want[4]))
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,vocab,k,how", [
+    (1, 1, 1, "plain"), (1, 2, 2, "plain"), (3, 7, 5, "odd"), (2, 64, 64, "plain"),
+    (4, 65, 64, "left"), (5, 2047, 20, "odd"), (1, 32000, 5, "plain"), (2, 50021, 64, "odd"),
+    (1, 131072, 64, "plain"), (7, 8193, 1, "plain"), (300, 3001, 20, "odd"),
+    (1030, 700, 3, "plain"), (1024, 9000, 64, "plain"), (3, 100000, 0, "plain")])
+def test_scores(kind, rows, vocab, k, how):
+    rng = np.random.default_rng(rows * vocab)
+    x = 3 * rng.standard_normal((rows, vocab))
+    ids = rng.integers(0, vocab, rows)
+    ids[rows // 2] = int(np.argmax(to_gpu(x[rows // 2], kind).float().cpu().numpy()))
+    check_scores(x, ids, kind, 0.8 if vocab % 2 else 1.0, k, how, f"{rows}x{vocab}")
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("vocab", [100, 5000, 40000])
+@pytest.mark.parametrize("shape", ["constant", "rising", "falling", "two_values", "steps"])
+def test_scores_with_ties_and_order(kind, vocab, shape):
+    """Orders and ties that the candidate lists meet at their worst."""
+    rng = np.random.default_rng(vocab)
+    x = {"constant": np.full((2, vocab), 1.25),
+         "rising": np.tile(np.linspace(-20, 20, vocab), (2, 1)),
+         "falling": np.tile(np.linspace(20, -20, vocab), (2, 1)),
+         "two_values": np.where(rng.random((2, vocab)) < 0.5, 1.0, -1.0),
+         "steps": np.tile(np.floor(np.arange(vocab) / 37) * 0.125, (2, 1))}[shape]
+    for k in (1, 20, 64):
+        check_scores(x, [vocab // 3, vocab - 1], kind, 1.0, k, "plain", f"{shape} {vocab} {k}")
+
+
+def test_scores_masks_and_special_values():
+    rng = np.random.default_rng(9)
+    x = rng.standard_normal((12, 9000)).astype(np.float32)
+    ids = rng.integers(0, 9000, 12)
+    x[0] = -np.inf                       # nothing allowed
+    x[1, 5:] = -np.inf                   # fewer allowed than asked for
+    x[2, rng.random(9000) < 0.9] = -np.inf
+    x[3] = -3.4028235e38                 # masked by the type's lowest value
+    x[4, 10:] = -3.4028235e38
+    x[5, 77] = np.nan
+    x[6, 78] = np.inf
+    x[7, :] = np.where(np.arange(9000) % 2, 0.0, -0.0)     # equal zeros of both signs
+    x[8] = 3e38 * np.sign(rng.standard_normal(9000))       # differences overflow
+    x[9, 4] = -np.inf
+    ids[9] = 4                           # the given token is masked
+    ids[1] = 100                         # so is this one, after and before others
+    ids[10], ids[11] = -1, 9000
+    for scale in (1.0, 0.3, 7.0):
+        check_scores(x, ids, "f32", scale, 20, "plain", f"special {scale}")
+    y = np.where(np.abs(x) > 6e4, np.sign(x) * 65504.0, x)
+    y[~np.isfinite(x)] = x[~np.isfinite(x)]
+    check_scores(y, ids, "f16", 1.0, 64, "odd", "special f16")
+
+
+def test_scores_of_empty_wide_and_without_ids():
+    import torch
+    from post_weight_quantization_layer_amd.scoring import TokenScorer
+    rng = np.random.default_rng(3)
+    x = to_gpu(rng.standard_normal((6, 70000)))
+    sc = TokenScorer(6, 70000, 64)
+    a = sc(x, torch.arange(6, device="cuda"))
+    first = [t.clone() for t in (a.entropy, a.top_ids, a.top_logprobs)]
+    b = sc(x)
+    assert b.logprob is None and b.rank is None
+    for u, v in zip(first, (b.entropy, b.top_ids, b.top_logprobs)):
+        assert torch.equal(u, v)                       # the same bits again
+    assert sc(x[:0], torch.zeros(0, dtype=torch.int64, device="cuda")).logprob.numel() == 0
+
+
+# ----------------------------------------------------- streams, graphs, path
+
+def small_mlp(rng, d=256, inner=384):
+    from post_weight_quantization_layer_amd.mlp import GatedMLP8
+    from post_weight_quantization_layer_amd.norms import NormBlock
+    w = [to_gpu(1 + 0.1 * rng.standard_normal(d), "f16") for _ in range(3)]
+    gu, dn = stored_layer(rng, 2 * inner, d), stored_layer(rng, d, inner)
+    mlp = GatedMLP8(NormBlock(d, pre="rms", pre_weight=w[0]), layer_on_gpu(*gu),
+                    layer_on_gpu(*dn), NormBlock(d, post="rms", post_weight=w[1], pre="rms",
+                                                 pre_weight=w[2], block_scale=0.5))
+    return mlp, w, gu, dn
+
+
+def test_gated_mlp_path():
+    """The block against its float64 composition.  The codes' roundings can flip
+    where a value lies on a half step, and one flip moves an output by a step's
+    share; so the bar is on the norm of the difference: the stored halves g, u
+    and b are rounded to float16 (2^-11 each) and the float32 parts are far
+    below, at most 4 * 2^-11 together with the output's own rounding."""
+    rng = np.random.default_rng(21)
+    mlp, w, gu, dn = small_mlp(rng)
+    r = to_gpu(activations(rng, 50, 256), "f16")
+    got_r, got_h = mlp(r)
+    r64 = back(r).astype(np.float64)
+    f = [back(v).astype(np.float64) for v in w]
+
+    def linear(x, layer):
+        q, s, _ = R.token_codes(x.astype(np.float32))
+        return R.product_sums(q, layer[0], layer[2]) * (s[:, None].astype(np.float64) * layer[1])
+
+    x = linear(R.norm(r64, "rms", f[0], None, 1e-6), gu)
+    b = linear(R.silu_mul(x[:, :384], x[:, 384:]), dn)
+    want_r, want_h = R.norm_block(r64, b, post="rms", post_weight=f[1], pre="rms",
+                                  pre_weight=f[2], block_scale=0.5, eps=1e-6)
+    for got, want in ((got_r, want_r), (got_h, want_h)):
+        rel = np.linalg.norm(back(got) - want) / np.linalg.norm(want)
+        log(f"gated mlp: relative difference {rel:.2e}")
+        assert rel <= 4 * 2.0 ** -11
+
+
+def test_on_two_streams_and_in_a_graph():
+    """The same bits on another stream and when replayed from a graph, with other
+    work and synchronizations between the replays."""
+    import torch
+    from post_weight_quantization_layer_amd.scoring import TokenScorer
+    rng = np.random.default_rng(22)
+    mlp, *_ = small_mlp(rng)
+    head = layer_on_gpu(*stored_layer(rng, 5000, 256))
+    scorer = TokenScorer(8, 5000, 10)
+    r = to_gpu(activations(rng, 8, 256), "f16")
+    ids = torch.arange(8, device="cuda") * 3
+    logits = torch.empty((8, 5000), dtype=torch.float32, device="cuda")
+
+    def step():
+        out, h = mlp(r)
+        return out, h, scorer(head(h, logits), ids)
+
+    out, h, s = step()
+    want = [t.clone() for t in (out, h, logits, s.logprob, s.rank, s.top_ids, s.entropy)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        out, h, s = step()
+        got = (out, h, logits, s.logprob, s.rank, s.top_ids, s.entropy)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out, h, s = step()
+    for i in range(4):
+        for t in got:
+            t.zero_()
+        eager = (r.float() * i).sum()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = (out, h, logits, s.logprob, s.rank, s.top_ids, s.entropy)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
