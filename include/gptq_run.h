@@ -111,8 +111,9 @@ size_t gptq_w8a8_linear_ws_bytes(const gptq_w8a8_layer *layer, int64_t tokens);
  * exact in int32, then one float32 product of it with scale[t] * w[r], then
  * one rounding to y's type (nearest, ties to even).
  *
- *  codes, ld_codes, scale, sum  as above, 1 <= tokens <= 2^20.  Bytes cols ..
- *         k_pad - 1 of a row of codes are read but do not matter.
+ *  codes, ld_codes, scale, sum  as above, ld_codes <= 2^22, tokens <= 2^20.
+ *         Bytes cols .. k_pad - 1 of a row of codes are read but do not
+ *         matter.
  *  y      tokens x rows of y_dtype, row stride ld_y.
  *  ws     scratch, 256-byte aligned, >= gptq_w8a8_gemm_ws_bytes.
  */

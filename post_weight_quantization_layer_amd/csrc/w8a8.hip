@@ -26,6 +26,7 @@ gptq_status check_activations(const void *x, int32_t dtype, int64_t tokens, int6
 namespace {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x4r_t __attribute__((ext_vector_type(4)));
 
 constexpr int kStep = 128;       // k per prepared tile
 
@@ -98,55 +99,241 @@ struct GemmArgs {
   int tokens, rows, row_tiles, steps, y_type;
 };
 
-// Outputs of one 16 x 16 result block: the lane's token t (column l % 16) and
-// four rows r .. r + 3 (4 (l / 16)).
-__device__ __forceinline__ void store_block(const GemmArgs &a, const i32x4_t &acc, int t, int r) {
-  if (t >= a.tokens || r >= a.rows) return;
-  const float st = a.x_scale[t];
-  const int sum = a.x_sum[t];
-  float v[4];
-  uint32_t n = a.rows - r;
+// Result blocks of a wave: acc[i][j] holds rows r0 + 16 i + 4 (l / 16) .. + 3
+// (registers) of token t0 + 16 j + l % 16 (l the lane).
+template <typename T, int FA, int FB>
+__device__ __forceinline__ void store_typed(const GemmArgs &a, const i32x4_t (&acc)[FA][FB],
+                                            int t0, int r0, int lane) {
+  float st[FB];
+  int sum[FB];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)       // rows_pad is a multiple of 16: in bounds
-    v[j] = float(int(uint32_t(acc[j]) - uint32_t(a.w_shift[r + j]) * uint32_t(sum))) *
-           (st * a.w_scale[r + j]);
-  const int64_t at = int64_t(t) * a.ld_y + r;
-  auto put = [&](auto tag) {
-    using T = decltype(tag);
-    T *p = static_cast<T *>(a.y) + at;
-    T o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = narrow<T>(v[j]);
-    if (n >= 4) __builtin_memcpy(p, o, sizeof(o));
-    else
-      for (uint32_t j = 0; j < n; ++j) p[j] = o[j];
-  };
-  if (a.y_type == GPTQ_DT_F32) put(float{});
-  else if (a.y_type == GPTQ_DT_BF16) put(bf16_t{});
-  else put(f16_t{});
-}
-
-// One wave per 16 rows x 64 tokens, operands straight from memory.
-__global__ void __launch_bounds__(256) w8a8_plain_kernel(GemmArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int rt = blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int t0 = blockIdx.y * 64;
-  if (rt >= a.row_tiles) return;
-  i32x4_t acc[4] = {};
-  const int8_t *w = a.w + int64_t(rt) * a.steps * 2048 + lane * 16;
-  for (int s = 0; s < 2 * a.steps; ++s) {
-    const i32x4_t wf = *reinterpret_cast<const i32x4_t *>(w + int64_t(s) * 1024);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = min(t0 + 16 * j + (lane & 15), a.tokens - 1);
-      const i32x4_t xf = *reinterpret_cast<const i32x4_t *>(a.x + int64_t(t) * a.ld_x + s * 64 +
-                                                            (lane >> 4) * 16);
-      acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf, xf, acc[j], 0, 0, 0);
-    }
+  for (int j = 0; j < FB; ++j) {
+    const int t = min(t0 + 16 * j + (lane & 15), a.tokens - 1);
+    st[j] = a.x_scale[t];
+    sum[j] = a.x_sum[t];
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    store_block(a, acc[j], t0 + 16 * j + (lane & 15), rt * 16 + 4 * (lane >> 4));
+  for (int i = 0; i < FA; ++i) {
+    const int r = r0 + 16 * i + 4 * (lane >> 4), left = a.rows - r;
+    if (left <= 0) continue;
+    // rows_pad is a multiple of 16, so all four are in bounds
+    const f32x4r_t ws = *reinterpret_cast<const f32x4r_t *>(a.w_scale + r);
+    const i32x4_t sh = *reinterpret_cast<const i32x4_t *>(a.w_shift + r);
+#pragma unroll
+    for (int j = 0; j < FB; ++j) {
+      const int t = t0 + 16 * j + (lane & 15);
+      if (t >= a.tokens) continue;
+      T o[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        float f = float(int(uint32_t(acc[i][j][v]) - uint32_t(sh[v]) * uint32_t(sum[j]))) *
+                  (st[j] * ws[v]);
+        // rounded to float32 before it is narrowed (not in one
+        // mixed-precision multiply)
+        asm("" : "+v"(f));
+        o[v] = narrow<T>(f);
+      }
+      T *p = static_cast<T *>(a.y) + int64_t(t) * a.ld_y + r;
+      if (left >= 4) {
+        __builtin_memcpy(p, o, sizeof(o));
+      } else {
+#pragma unroll
+        for (int v = 0; v < 3; ++v)
+          if (v < left) p[v] = o[v];
+      }
+    }
+  }
+}
+template <int FA, int FB>
+__device__ __forceinline__ void store_blocks(const GemmArgs &a, const i32x4_t (&acc)[FA][FB],
+                                             int t0, int r0, int lane) {
+  if (a.y_type == GPTQ_DT_F32) store_typed<float>(a, acc, t0, r0, lane);
+  else if (a.y_type == GPTQ_DT_BF16) store_typed<bf16_t>(a, acc, t0, r0, lane);
+  else store_typed<f16_t>(a, acc, t0, r0, lane);
+}
+
+// ---- Tiles through LDS.  A workgroup of 4 waves (2 x 2) makes a tile of
+// 32 FA rows x 32 FB tokens; a wave FA x FB blocks of 16 x 16.  Stages of
+// 128 k are double-buffered in LDS: weights in the prepared order (a
+// fragment is 1 KiB of consecutive LDS), tokens as 128-byte rows whose
+// 16-byte pieces are XOR-swizzled; both read without bank conflicts.
+//
+// Iteration u: step 0 multiplies the first 64 k of stage u (set X) while the
+// second 64 k (set Y) are read; a barrier makes stage u + 1 visible; step 1
+// multiplies set Y while set X is read from stage u + 1.  Each of a stage's
+// copies waits in a register from its load to its store one to two steps
+// later, into the ring slot whose last reads came before the previous
+// barrier.
+__device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
+
+// Tiles in bands of kBand token tiles, tokens fastest: workgroups are dealt
+// round-robin to the 8 XCDs, each XCD takes a contiguous run of this order,
+// so its 32 concurrent tiles share 4 token and 8 row panels in its L2.
+constexpr int kBand = 4;
+__device__ __forceinline__ void tile_at(int bid, int tt, int rt, int &t, int &r) {
+  const int n = tt * rt, x = bid & 7;
+  const int at = x * (n / 8) + min(x, n % 8) + (bid >> 3);
+  const int band = at / (kBand * rt), b0 = band * kBand, h = min(kBand, tt - b0);
+  const int u = at - b0 * rt;
+  r = __builtin_amdgcn_readfirstlane(u / h);    // wave-uniform, kept scalar
+  t = __builtin_amdgcn_readfirstlane(b0 + u % h);
+}
+
+// acc += w x^T on the matrix core, in place in accumulation registers.  (The
+// builtin leaves the result's register free; with every accumulation register
+// taken, the compiler then moved whole accumulators between files in the
+// loop.)  The operands come from LDS reads, never straight from vector ALU
+// instructions, and acc is next touched 16 or more of these later; after the
+// last one, and before the first, settle() waits the pipeline out.
+__device__ __forceinline__ void mfma_acc(i32x4_t &acc, i32x4_t w, i32x4_t x) {
+  asm("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(w), "v"(x));
+}
+template <int FA, int FB>
+__device__ __forceinline__ void settle(i32x4_t (&acc)[FA][FB]) {
+#pragma unroll
+  for (int i = 0; i < FA; ++i)
+#pragma unroll
+    for (int j = 0; j < FB; ++j) asm volatile("" : "+a"(acc[i][j]));
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15\n\ts_nop 15");
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < FA; ++i)
+#pragma unroll
+    for (int j = 0; j < FB; ++j) asm volatile("" : "+a"(acc[i][j]));
+}
+
+template <int FA, int FB>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FA * FB > 16 ? 1 : 2)))
+    w8a8_tile_kernel(GemmArgs a, int token_tiles, int row_tiles) {
+  constexpr int kWBytes = 32 * FA * kStep, kXBytes = 32 * FB * kStep;
+  constexpr int kStageBytes = kWBytes + kXBytes;
+  constexpr int kWLoads = FA, kLoads = FA + FB;     // 16-byte copies per lane and stage
+  constexpr int kHalf = kLoads / 2;
+  constexpr int kSlots = FA * FB;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  int tt, tr;
+  tile_at(blockIdx.x, token_tiles, row_tiles, tt, tr);
+  const int rt0 = tr * 2 * FA, t0 = tt * 32 * FB;   // first 16-row tile, first token
+  const int U = a.steps;
+
+  // Copy q of a lane: 4 KiB of weights (two 16-row tiles) or 32 token rows.
+  // Rows past the layer or the tokens are clamped; they only feed outputs
+  // that are never stored.
+  const int8_t *wbase = a.w + int64_t(rt0) * a.steps * 2048;
+  const int8_t *xbase = a.x + int64_t(t0) * a.ld_x;
+  uint32_t voff[kLoads];
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q) {
+    if (q < kWLoads)
+      voff[q] = uint32_t(min(2 * q + (tid >> 7), a.row_tiles - 1 - rt0)) * uint32_t(a.steps * 2048) +
+                (tid & 127) * 16;
+    else
+      voff[q] = uint32_t(min(32 * (q - kWLoads) + (tid >> 3), a.tokens - 1 - t0)) *
+                    uint32_t(a.ld_x) + (tid & 7) * 16;
+  }
+  const int xrow = tid >> 3;
+  const int lds_x = kWBytes + xrow * kStep + (((tid & 7) ^ swz(xrow)) << 4);
+  u32x4r_t stg[kLoads];
+  auto load_one = [&](int q, int t) {
+    t = min(t, U - 1);
+    auto base = (const __attribute__((address_space(1))) int8_t *)(
+        q < kWLoads ? wbase + int64_t(t) * 2048 : xbase + int64_t(t) * kStep);
+    uint32_t off = voff[q];
+    asm("" : "+s"(base), "+v"(off));   // scalar base, the lane's fixed 32-bit offset
+    stg[q] = *(const __attribute__((address_space(1))) u32x4r_t *)(base + off);
+  };
+  auto store_one = [&](int q, int t) {
+    uint8_t *p = smem + (t & 1) * kStageBytes +
+                 (q < kWLoads ? q * 4096 + tid * 16 : lds_x + (q - kWLoads) * 32 * kStep);
+    *reinterpret_cast<u32x4r_t *>(p) = stg[q];
+  };
+  auto frag_a = [&](int u, int h, int i) {
+    return *reinterpret_cast<const i32x4_t *>(smem + (u & 1) * kStageBytes +
+                                              (wm * FA + i) * 2048 + h * 1024 + lane * 16);
+  };
+  auto frag_b = [&](int u, int h, int j) {
+    const int row = wn * 16 * FB + 16 * j + (lane & 15), c = 4 * h + (lane >> 4);
+    return *reinterpret_cast<const i32x4_t *>(smem + (u & 1) * kStageBytes + kWBytes +
+                                              row * kStep + ((c ^ swz(row)) << 4));
+  };
+
+  i32x4_t acc[FA][FB];
+#pragma unroll
+  for (int i = 0; i < FA; ++i)
+#pragma unroll
+    for (int j = 0; j < FB; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+  i32x4_t xa[4], xb[FB], ya[FA], yb[FB];   // xa: block row i in slot i % 4
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q) load_one(q, 0);
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q) {
+    store_one(q, 0);
+    load_one(q, 1);
+  }
+#pragma unroll
+  for (int q = 0; q < kHalf; ++q) {
+    store_one(q, 1);
+    load_one(q, 2);
+  }
+  __builtin_amdgcn_s_waitcnt(0xc07f);      // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+#pragma unroll
+  for (int j = 0; j < FB; ++j) xb[j] = frag_b(0, 0, j);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) xa[i] = frag_a(0, 0, i);
+
+  settle<FA, FB>(acc);   // the zeros are written well before the first MFMA reads them
+
+  constexpr int kY = FA + FB, kYEvery = kSlots / kY;       // reads of set Y in step 0
+  constexpr int kX = FB + 3, kXEvery = kSlots / kX;        // reads of set X in step 1
+  constexpr int kCEvery = kSlots / kHalf;                  // copies in either step
+  for (int u = 0; u < U; ++u) {
+#pragma unroll
+    for (int i = 0; i < FA; ++i)
+#pragma unroll
+      for (int j = 0; j < FB; ++j) {
+        mfma_acc(acc[i][j], xa[i % 4], xb[j]);
+        const int q = FB * i + j;
+        if (j == 1 && i + 3 < FA) xa[(i + 3) % 4] = frag_a(u, 0, i + 3);
+        if (q % kYEvery == kYEvery / 2 && q / kYEvery < kY) {
+          const int f = q / kYEvery;
+          if (f == 0) ya[0] = frag_a(u, 1, 0);
+          else if (f <= FB) yb[f - 1] = frag_b(u, 1, f - 1);
+          else ya[f - FB] = frag_a(u, 1, f - FB);
+        }
+        if (q % kCEvery == kCEvery - 1 && q / kCEvery < kHalf) {
+          store_one(kHalf + q / kCEvery, u + 1);
+          load_one(kHalf + q / kCEvery, u + 2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    __builtin_amdgcn_s_waitcnt(0xc07f);    // lgkmcnt(0): stores of u + 1, reads of u done
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < FA; ++i)
+#pragma unroll
+      for (int j = 0; j < FB; ++j) {
+        mfma_acc(acc[i][j], ya[i], yb[j]);
+        const int q = FB * i + j;
+        if (q % kXEvery == kXEvery / 2 && q / kXEvery < kX) {
+          const int f = q / kXEvery;
+          if (f < FB) xb[f] = frag_b(u + 1, 0, f);
+          else xa[f - FB] = frag_a(u + 1, 0, f - FB);
+        }
+        if (q % kCEvery == kCEvery - 1 && q / kCEvery < kHalf) {
+          store_one(q / kCEvery, u + 2);
+          load_one(q / kCEvery, u + 3);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+  }
+  settle<FA, FB>(acc);
+  store_blocks<FA, FB>(a, acc, t0 + wn * 16 * FB, (rt0 + wm * FA) * 16, lane);
 }
 
 constexpr int64_t kMaxRows = int64_t(1) << 24, kMaxTokens = int64_t(1) << 20;
@@ -185,6 +372,15 @@ gptq_status check_scratch(const void *ws, size_t ws_bytes, size_t need) {
   return GPTQ_OK;
 }
 
+template <int FA, int FB>
+gptq_status launch_tiles(const GemmArgs &a, hipStream_t s) {
+  auto kern = w8a8_tile_kernel<FA, FB>;
+  const size_t lds = size_t(2) * 32 * (FA + FB) * kStep;
+  GPTQ_TRY(allow_dynamic_lds(reinterpret_cast<const void *>(kern), lds));
+  const int rt = int(cdiv(a.rows, 32 * FA)), tt = int(cdiv(a.tokens, 32 * FB));
+  return launch("w8a8_gemm", kern, dim3(uint32_t(rt) * uint32_t(tt)), dim3(256), lds, s, a, tt, rt);
+}
+
 gptq_status gemm_launch(const gptq_w8a8_layer *l, const int8_t *codes, int64_t ld_codes,
                         const float *scale, const int32_t *sum, int64_t tokens, void *y,
                         int32_t y_dtype, int64_t ld_y, void *ws, hipStream_t s) {
@@ -205,9 +401,12 @@ gptq_status gemm_launch(const gptq_w8a8_layer *l, const int8_t *codes, int64_t l
   a.row_tiles = int(g.rows_pad / 16);
   a.steps = int(g.k_pad / kStep);
   a.y_type = y_dtype;
-  return launch("w8a8_gemm", w8a8_plain_kernel,
-                dim3(uint32_t(cdiv(a.row_tiles, 4)), uint32_t(cdiv(tokens, 64))), dim3(256), 0, s,
-                a);
+  const int cus = device_cu_count();
+  const int64_t big = cdiv(g.rows, 256) * cdiv(tokens, 256);
+  if (big >= cus) return launch_tiles<8, 8>(a, s);
+  const int64_t mid = cdiv(g.rows, 128) * cdiv(tokens, 256);
+  if (mid >= cus && tokens >= 192) return launch_tiles<4, 8>(a, s);
+  return launch_tiles<4, 4>(a, s);
 }
 
 }  // namespace
@@ -272,10 +471,11 @@ gptq_status gptq_w8a8_gemm(const gptq_w8a8_layer *layer, const int8_t *codes, in
     if (tokens == 0) return GPTQ_OK;
     if (!codes || !scale || !sum)
       return fail(GPTQ_ERR_INVALID_ARG, "codes, scale and sum must not be NULL");
-    if (!aligned_to(codes, 16) || ld_codes % 16 || ld_codes < layer->k_pad)
+    if (!aligned_to(codes, 16) || ld_codes % 16 || ld_codes < layer->k_pad ||
+        ld_codes > (int64_t(1) << 22))
       return fail(GPTQ_ERR_INVALID_ARG,
-                  "codes must be 16-byte aligned, ld_codes a multiple of 16 and >= "
-                  "gptq_tokens_ld(cols)");
+                  "codes must be 16-byte aligned, ld_codes a multiple of 16 in "
+                  "[gptq_tokens_ld(cols), 2^22]");
     if (!aligned_to(scale, 4) || !aligned_to(sum, 4))
       return fail(GPTQ_ERR_INVALID_ARG, "scale and sum must be 4-byte aligned");
     GPTQ_TRY(check_output(layer, y, y_dtype, ld_y));
