@@ -97,6 +97,7 @@ struct GemmArgs {
   void *y;
   int64_t ld_x, ld_y;
   int tokens, rows, row_tiles, steps, y_type;
+  i32x4_t *part;    // split products: the blocks of each (tile, split)
 };
 
 // Result blocks of a wave: acc[i][j] holds rows r0 + 16 i + 4 (l / 16) .. + 3
@@ -152,6 +153,14 @@ __device__ __forceinline__ void store_blocks(const GemmArgs &a, const i32x4_t (&
   else store_typed<f16_t>(a, acc, t0, r0, lane);
 }
 
+// A workgroup barrier that orders LDS accesses only: loads from memory stay
+// in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // ---- Tiles through LDS.  A workgroup of 4 waves (2 x 2) makes a tile of
 // 32 FA rows x 32 FB tokens; a wave FA x FB blocks of 16 x 16.  Stages of
 // 128 k are double-buffered in LDS: weights in the prepared order (a
@@ -203,9 +212,9 @@ __device__ __forceinline__ void settle(i32x4_t (&acc)[FA][FB]) {
     for (int j = 0; j < FB; ++j) asm volatile("" : "+a"(acc[i][j]));
 }
 
-template <int FA, int FB>
+template <int FA, int FB, bool SPLIT>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FA * FB > 16 ? 1 : 2)))
-    w8a8_tile_kernel(GemmArgs a, int token_tiles, int row_tiles) {
+    w8a8_tile_kernel(GemmArgs a, int token_tiles, int row_tiles, int splits) {
   constexpr int kWBytes = 32 * FA * kStep, kXBytes = 32 * FB * kStep;
   constexpr int kStageBytes = kWBytes + kXBytes;
   constexpr int kWLoads = FA, kLoads = FA + FB;     // 16-byte copies per lane and stage
@@ -216,15 +225,19 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FA 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   int tt, tr;
-  tile_at(blockIdx.x, token_tiles, row_tiles, tt, tr);
+  const int tiles = token_tiles * row_tiles;
+  const int split = SPLIT ? int(blockIdx.x) / tiles : 0;
+  const int tile = int(blockIdx.x) - split * tiles;
+  tile_at(tile, token_tiles, row_tiles, tt, tr);
   const int rt0 = tr * 2 * FA, t0 = tt * 32 * FB;   // first 16-row tile, first token
-  const int U = a.steps;
+  const int s0 = SPLIT ? a.steps * split / splits : 0;
+  const int U = SPLIT ? a.steps * (split + 1) / splits - s0 : a.steps;
 
   // Copy q of a lane: 4 KiB of weights (two 16-row tiles) or 32 token rows.
   // Rows past the layer or the tokens are clamped; they only feed outputs
   // that are never stored.
-  const int8_t *wbase = a.w + int64_t(rt0) * a.steps * 2048;
-  const int8_t *xbase = a.x + int64_t(t0) * a.ld_x;
+  const int8_t *wbase = a.w + (int64_t(rt0) * a.steps + s0) * 2048;
+  const int8_t *xbase = a.x + int64_t(t0) * a.ld_x + s0 * kStep;
   uint32_t voff[kLoads];
 #pragma unroll
   for (int q = 0; q < kLoads; ++q) {
@@ -279,8 +292,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FA 
     store_one(q, 1);
     load_one(q, 2);
   }
-  __builtin_amdgcn_s_waitcnt(0xc07f);      // lgkmcnt(0)
-  __builtin_amdgcn_s_barrier();
+  lds_barrier();
 #pragma unroll
   for (int j = 0; j < FB; ++j) xb[j] = frag_b(0, 0, j);
 #pragma unroll
@@ -311,8 +323,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FA 
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-    __builtin_amdgcn_s_waitcnt(0xc07f);    // lgkmcnt(0): stores of u + 1, reads of u done
-    __builtin_amdgcn_s_barrier();
+    lds_barrier();                         // stores of u + 1, reads of u done
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < FA; ++i)
@@ -333,7 +344,214 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FA 
       }
   }
   settle<FA, FB>(acc);
+  if (SPLIT) {
+    // A wave's blocks as they lie in its registers: 1 KiB per store.
+    i32x4_t *p = a.part + (int64_t(tile) * splits + split) * (4 * FA * FB * 64) +
+                 wave * (FA * FB * 64) + lane;
+#pragma unroll
+    for (int i = 0; i < FA; ++i)
+#pragma unroll
+      for (int j = 0; j < FB; ++j) p[(i * FB + j) * 64] = acc[i][j];
+    return;
+  }
   store_blocks<FA, FB>(a, acc, t0 + wn * 16 * FB, (rt0 + wm * FA) * 16, lane);
+}
+
+// Adds a split product's parts: a wave per block row (FB blocks) of a tile's
+// wave, in the tile kernel's register order.
+template <int FA, int FB>
+__global__ void __launch_bounds__(256)
+    w8a8_join_kernel(GemmArgs a, int token_tiles, int row_tiles, int splits) {
+  const int lane = threadIdx.x & 63;
+  const int unit = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  const int i = unit % FA, wave = unit / FA % 4, tile = unit / (4 * FA);
+  int tt, tr;
+  tile_at(tile, token_tiles, row_tiles, tt, tr);
+  const int r0 = (tr * 2 * FA + (wave >> 1) * FA + i) * 16;
+  const int t0 = tt * 32 * FB + (wave & 1) * 16 * FB;
+  if (r0 >= a.rows || t0 >= a.tokens) return;
+  const i32x4_t *p = a.part + int64_t(tile) * splits * (4 * FA * FB * 64) +
+                     (wave * FA + i) * (FB * 64) + lane;
+  i32x4_t acc[1][FB];
+#pragma unroll
+  for (int j = 0; j < FB; ++j) acc[0][j] = p[j * 64];
+  for (int s = 1; s < splits; ++s) {
+    p += 4 * FA * FB * 64;
+#pragma unroll
+    for (int j = 0; j < FB; ++j) acc[0][j] += p[j * 64];
+  }
+  store_blocks<1, FB>(a, acc, t0, r0, lane);
+}
+
+// ---- Few tokens: a workgroup per 16 rows, its waves splitting k.  A wave
+// takes every WAVES-th 128-k step: its weights come straight from memory as
+// contiguous KiB, several steps ahead, and each is used for all tokens at
+// once, so the product runs at the rate the weights arrive.  The waves'
+// sums meet in LDS.
+//
+// Tokens come as codes from memory (every workgroup reads them all, from its
+// XCD's L2), or, FUSED, as activations that each workgroup quantizes into LDS
+// itself while its first weights are on their way: that repeats a small
+// quantization per 16 rows but saves a launch.
+// Steps loaded at a time, two such sets in flight: what fits 128 registers a
+// lane with 16 waves (256 with fewer) beside the tokens' codes.
+constexpr int ahead(int waves, int nb, bool fused) {
+  return fused ? 4 : nb == 1 ? (waves == 16 ? 2 : 4) : (waves == 16 ? 1 : 2);
+}
+constexpr int kFusedChunks = 4;  // 8-element chunks of activations a lane may hold
+
+struct RowsFused {
+  const void *x;
+  int64_t ld;
+  int cols;
+};
+
+template <typename T, int WAVES, int NB, bool FUSED>
+__global__ void __launch_bounds__(64 * WAVES) w8a8_rows_kernel(GemmArgs a, RowsFused f) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kThreads = 64 * WAVES, kAhead = ahead(WAVES, NB, FUSED);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rt = blockIdx.x;
+  const int k_pad = a.steps * kStep, ld_lds = k_pad + 16;
+  i32x4_t *sums = reinterpret_cast<i32x4_t *>(smem);                    // WAVES x NB KiB
+  int8_t *codes = reinterpret_cast<int8_t *>(smem + WAVES * NB * 1024);  // FUSED: tokens rows
+  __shared__ uint32_t slot_max[16][WAVES];
+  __shared__ int slot_sum[16][WAVES];
+
+  // This wave's steps: wave, wave + WAVES, ...  Loads past the last repeat it.
+  const int n = (a.steps - wave + WAVES - 1) / WAVES;
+  const int8_t *w = a.w + int64_t(rt) * a.steps * 2048 + lane * 16;
+  const int8_t *xrow[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int t = min(16 * j + (lane & 15), a.tokens - 1);
+    xrow[j] = FUSED ? codes + t * ld_lds + (lane >> 4) * 16
+                    : a.x + int64_t(t) * a.ld_x + (lane >> 4) * 16;
+  }
+  struct Set {
+    i32x4_t w[kAhead][2], x[FUSED ? 1 : kAhead][2][NB];
+  };
+  auto load = [&](Set &b, int at) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t s = wave + int64_t(min(at + i, n - 1)) * WAVES;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        b.w[i][h] = *reinterpret_cast<const i32x4_t *>(w + s * 2048 + h * 1024);
+        if (!FUSED)
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+            b.x[FUSED ? 0 : i][h][j] =
+                *reinterpret_cast<const i32x4_t *>(xrow[j] + s * kStep + h * 64);
+      }
+    }
+  };
+  i32x4_t acc[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) acc[j] = i32x4_t{0, 0, 0, 0};
+  auto multiply = [&](const Set &b, int at) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (at + i >= n) break;
+      const int s = wave + (at + i) * WAVES;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const i32x4_t xf = FUSED ? *reinterpret_cast<const i32x4_t *>(xrow[j] + s * kStep + h * 64)
+                                   : b.x[FUSED ? 0 : i][h][j];
+          acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b.w[i][h], xf, acc[j], 0, 0, 0);
+        }
+    }
+  };
+  Set s0, s1;
+  if (n > 0) {
+    load(s0, 0);
+    load(s1, kAhead);
+  }
+  if (FUSED) {
+    // Chunk c of a lane: token c / per, elements 8 (c % per * threads + tid).
+    const int per = (k_pad + 8 * kThreads - 1) / (8 * kThreads);
+    float v[kFusedChunks][8];
+#pragma unroll
+    for (int c = 0; c < kFusedChunks; ++c) {
+      const int t = c / per, e0 = 8 * (c % per * kThreads + tid);
+      if (t < a.tokens)
+        load8(static_cast<const T *>(f.x) + t * f.ld + min(e0, f.cols - 1), f.cols - e0, v[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < kFusedChunks; ++c) {
+      const int t = c / per;
+      if (t >= a.tokens) break;
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = MaxU::op(m, __float_as_uint(v[c][j]) & 0x7fffffffu);
+      m = wave_all<MaxU>(m);
+      if (lane == 0) slot_max[c][wave] = m;
+    }
+    lds_barrier();
+#pragma unroll
+    for (int c = 0; c < kFusedChunks; ++c) {
+      const int t = c / per, e0 = 8 * (c % per * kThreads + tid);
+      if (t >= a.tokens) break;
+      uint32_t m = 0;
+      for (int p = 0; p < per; ++p)
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) m = MaxU::op(m, slot_max[t * per + p][i]);
+      const float s = row_scale(m);
+      int q[8] = {0, 0, 0, 0, 0, 0, 0, 0}, total = 0;
+      if (s > 0.f) codes8(v[c], s, 1.f / s, q);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) total += q[j];
+      if (e0 < k_pad) *reinterpret_cast<u32x2_t *>(codes + t * ld_lds + e0) = pack_codes8(q);
+      total = wave_all<SumI>(total);
+      if (lane == 0) slot_sum[c][wave] = total;
+    }
+    lds_barrier();
+  }
+  for (int at = 0; at < n; at += 2 * kAhead) {
+    multiply(s0, at);
+    if (at + 2 * kAhead < n) load(s0, at + 2 * kAhead);
+    multiply(s1, at + kAhead);
+    if (at + 3 * kAhead < n) load(s1, at + 3 * kAhead);
+  }
+#pragma unroll
+  for (int j = 0; j < NB; ++j) sums[(wave * NB + j) * 64 + lane] = acc[j];
+  lds_barrier();
+  // Output (token, row) of thread: 16 consecutive rows per token.
+  const int *flat = reinterpret_cast<const int *>(sums);
+  for (int o = tid; o < 16 * a.tokens; o += kThreads) {
+    const int t = o >> 4, r = o & 15, row = rt * 16 + r;
+    // block t / 16: lane 16 (r / 4) + t % 16 holds rows 4 (r / 4) ..
+    const int at = (t >> 4) * 256 + (16 * (r >> 2) + (t & 15)) * 4 + (r & 3);
+    uint32_t total = 0;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) total += uint32_t(flat[i * NB * 256 + at]);
+    float st;
+    uint32_t sum = 0;
+    if (FUSED) {
+      const int per = (k_pad + 8 * kThreads - 1) / (8 * kThreads);
+      uint32_t m = 0;
+      for (int p = 0; p < per; ++p)
+#pragma unroll
+        for (int i = 0; i < WAVES; ++i) {
+          m = MaxU::op(m, slot_max[t * per + p][i]);
+          sum += uint32_t(slot_sum[t * per + p][i]);
+        }
+      st = row_scale(m);
+    } else {
+      st = a.x_scale[t];
+      sum = uint32_t(a.x_sum[t]);
+    }
+    if (row >= a.rows) continue;
+    float y = float(int(total - uint32_t(a.w_shift[row]) * sum)) * (st * a.w_scale[row]);
+    asm("" : "+v"(y));    // rounded to float32 before it is narrowed
+    const int64_t to = int64_t(t) * a.ld_y + row;
+    if (a.y_type == GPTQ_DT_F32) static_cast<float *>(a.y)[to] = y;
+    else if (a.y_type == GPTQ_DT_BF16) static_cast<bf16_t *>(a.y)[to] = narrow<bf16_t>(y);
+    else static_cast<f16_t *>(a.y)[to] = narrow<f16_t>(y);
+  }
 }
 
 constexpr int64_t kMaxRows = int64_t(1) << 24, kMaxTokens = int64_t(1) << 20;
@@ -372,41 +590,120 @@ gptq_status check_scratch(const void *ws, size_t ws_bytes, size_t need) {
   return GPTQ_OK;
 }
 
-template <int FA, int FB>
-gptq_status launch_tiles(const GemmArgs &a, hipStream_t s) {
-  auto kern = w8a8_tile_kernel<FA, FB>;
+// ------------------------------------------------------------- launch rules
+// How a product of `tokens` tokens runs: on the rows kernel (waves > 0), or
+// on tiles of 32 fa rows x 32 fb tokens, k in `splits` parts.
+struct Plan {
+  int waves, fa, fb, splits;
+};
+
+Plan plan_for(const Geometry &g, int64_t tokens, int cus) {
+  const int steps = int(g.k_pad / kStep);
+  if (tokens <= 32) {
+    // Enough waves to hold a row tile's k in flight; fewer, smaller
+    // workgroups where there are many row tiles.
+    const int64_t rt = g.rows_pad / 16;
+    int waves = rt >= 4 * cus ? 4 : rt >= 2 * cus ? 8 : 16;
+    while (waves < 16 && steps > waves * 16) waves *= 2;
+    while (waves > 4 && steps <= waves * 2) waves /= 2;
+    return {waves, 0, 0, 1};
+  }
+  const int64_t big = cdiv(g.rows, 256) * cdiv(tokens, 256);
+  if (big >= cus) return {0, 8, 8, 1};
+  const int64_t mid = cdiv(g.rows, 128) * cdiv(tokens, 256);
+  if (mid >= cus && tokens >= 192) return {0, 4, 8, 1};
+  if (tokens <= 64) {
+    const int64_t tiles = cdiv(g.rows, 128);
+    return {0, 4, 2, int(std::max<int64_t>(1, std::min<int64_t>(2 * cus / tiles, steps / 4)))};
+  }
+  const int64_t tiles = cdiv(g.rows, 128) * cdiv(tokens, 128);
+  return {0, 4, 4, int(std::max<int64_t>(1, std::min<int64_t>(2 * cus / tiles, steps / 4)))};
+}
+
+size_t part_bytes(const Geometry &g, int64_t tokens, const Plan &p) {
+  if (p.waves || p.splits == 1) return 0;
+  return align256(size_t(cdiv(g.rows, 32 * p.fa) * cdiv(tokens, 32 * p.fb)) * p.splits *
+                  (32 * p.fa * 32 * p.fb * sizeof(int32_t)));
+}
+
+template <int FA, int FB, bool SPLIT>
+gptq_status launch_tiles(const GemmArgs &a, int splits, hipStream_t s) {
+  auto kern = w8a8_tile_kernel<FA, FB, SPLIT>;
   const size_t lds = size_t(2) * 32 * (FA + FB) * kStep;
   GPTQ_TRY(allow_dynamic_lds(reinterpret_cast<const void *>(kern), lds));
   const int rt = int(cdiv(a.rows, 32 * FA)), tt = int(cdiv(a.tokens, 32 * FB));
-  return launch("w8a8_gemm", kern, dim3(uint32_t(rt) * uint32_t(tt)), dim3(256), lds, s, a, tt, rt);
+  const uint32_t tiles = uint32_t(rt) * uint32_t(tt);
+  GPTQ_TRY(launch("w8a8_gemm", kern, dim3(tiles * splits), dim3(256), lds, s, a, tt, rt, splits));
+  if (!SPLIT) return GPTQ_OK;
+  return launch("w8a8_join", w8a8_join_kernel<FA, FB>, dim3(tiles * FA), dim3(256), 0, s, a, tt,
+                rt, splits);
 }
 
-gptq_status gemm_launch(const gptq_w8a8_layer *l, const int8_t *codes, int64_t ld_codes,
-                        const float *scale, const int32_t *sum, int64_t tokens, void *y,
-                        int32_t y_dtype, int64_t ld_y, void *ws, hipStream_t s) {
-  const Geometry g = geometry(l->rows, l->cols);
+template <typename T, int WAVES, int NB, bool FUSED>
+gptq_status launch_rows(const GemmArgs &a, const RowsFused &f, hipStream_t s) {
+  auto kern = w8a8_rows_kernel<T, WAVES, NB, FUSED>;
+  const size_t lds = size_t(WAVES) * NB * 1024 +
+                     (FUSED ? size_t(a.tokens) * (a.steps * kStep + 16) : 0);
+  GPTQ_TRY(allow_dynamic_lds(reinterpret_cast<const void *>(kern), 96 * 1024));
+  return launch("w8a8_rows", kern, dim3(uint32_t(a.row_tiles)), dim3(64 * WAVES), lds, s, a, f);
+}
+template <typename T, int NB, bool FUSED>
+gptq_status launch_rows_waves(const GemmArgs &a, const RowsFused &f, int waves, hipStream_t s) {
+  if (waves == 4) return launch_rows<T, 4, NB, FUSED>(a, f, s);
+  if (waves == 8) return launch_rows<T, 8, NB, FUSED>(a, f, s);
+  return launch_rows<T, 16, NB, FUSED>(a, f, s);
+}
+
+// Whether each workgroup quantizes the activations itself: all tokens' chunks
+// fit in a lane's registers (then their codes, at most 4 * 8 * threads bytes,
+// fit in LDS too).
+bool fused_fits(const Geometry &g, int64_t tokens, const Plan &p) {
+  return p.waves && tokens * cdiv(g.k_pad, 8 * 64 * p.waves) <= kFusedChunks;
+}
+
+GemmArgs layer_args(const gptq_w8a8_layer *l, const Geometry &g, int64_t tokens, void *y,
+                    int32_t y_dtype, int64_t ld_y) {
   const LayerMap m = layer_map(l->mem, g);
   GemmArgs a;
   a.w = m.w;
   a.w_scale = m.scale;
   a.w_shift = m.shift;
-  a.x = codes;
-  a.x_scale = scale;
-  a.x_sum = sum;
+  a.x = nullptr;
+  a.x_scale = nullptr;
+  a.x_sum = nullptr;
   a.y = y;
-  a.ld_x = ld_codes;
+  a.ld_x = 0;
   a.ld_y = ld_y;
   a.tokens = int(tokens);
   a.rows = int(g.rows);
   a.row_tiles = int(g.rows_pad / 16);
   a.steps = int(g.k_pad / kStep);
   a.y_type = y_dtype;
-  const int cus = device_cu_count();
-  const int64_t big = cdiv(g.rows, 256) * cdiv(tokens, 256);
-  if (big >= cus) return launch_tiles<8, 8>(a, s);
-  const int64_t mid = cdiv(g.rows, 128) * cdiv(tokens, 256);
-  if (mid >= cus && tokens >= 192) return launch_tiles<4, 8>(a, s);
-  return launch_tiles<4, 4>(a, s);
+  a.part = nullptr;
+  return a;
+}
+
+gptq_status gemm_launch(const gptq_w8a8_layer *l, const int8_t *codes, int64_t ld_codes,
+                        const float *scale, const int32_t *sum, int64_t tokens, void *y,
+                        int32_t y_dtype, int64_t ld_y, void *ws, hipStream_t s) {
+  const Geometry g = geometry(l->rows, l->cols);
+  GemmArgs a = layer_args(l, g, tokens, y, y_dtype, ld_y);
+  a.x = codes;
+  a.x_scale = scale;
+  a.x_sum = sum;
+  a.ld_x = ld_codes;
+  a.part = static_cast<i32x4_t *>(ws);
+  const Plan p = plan_for(g, tokens, device_cu_count());
+  if (p.waves)
+    return tokens <= 16 ? launch_rows_waves<f16_t, 1, false>(a, RowsFused{}, p.waves, s)
+                        : launch_rows_waves<f16_t, 2, false>(a, RowsFused{}, p.waves, s);
+  if (p.fa == 8) return launch_tiles<8, 8, false>(a, 1, s);
+  if (p.fb == 8) return launch_tiles<4, 8, false>(a, 1, s);
+  if (p.fb == 2)
+    return p.splits > 1 ? launch_tiles<4, 2, true>(a, p.splits, s)
+                        : launch_tiles<4, 2, false>(a, 1, s);
+  return p.splits > 1 ? launch_tiles<4, 4, true>(a, p.splits, s)
+                      : launch_tiles<4, 4, false>(a, 1, s);
 }
 
 }  // namespace
@@ -450,13 +747,17 @@ gptq_status gptq_w8a8_prepare(const uint8_t *q, const float *scale, const uint8_
 }
 
 size_t gptq_w8a8_gemm_ws_bytes(const gptq_w8a8_layer *layer, int64_t tokens) {
-  return 0;
+  if (!layer || tokens < 1 || tokens > kMaxTokens) return 0;
+  const Geometry g = geometry(layer->rows, layer->cols);
+  return part_bytes(g, tokens, plan_for(g, tokens, device_cu_count()));
 }
 
 // The token codes, their scales and their sums come before the product's own
 // scratch.
 size_t gptq_w8a8_linear_ws_bytes(const gptq_w8a8_layer *layer, int64_t tokens) {
   if (!layer || tokens < 1 || tokens > kMaxTokens) return 0;
+  const Geometry g = geometry(layer->rows, layer->cols);
+  if (fused_fits(g, tokens, plan_for(g, tokens, device_cu_count()))) return 0;
   return codes_bytes(layer, tokens) + 2 * align256(size_t(tokens) * 4) +
          gptq_w8a8_gemm_ws_bytes(layer, tokens);
 }
@@ -495,13 +796,22 @@ gptq_status gptq_w8a8_linear(const gptq_w8a8_layer *layer, const void *x, int32_
     if (tokens == 0) return GPTQ_OK;
     GPTQ_TRY(check_output(layer, y, y_dtype, ld_y));
     GPTQ_TRY(check_scratch(ws, ws_bytes, gptq_w8a8_linear_ws_bytes(layer, tokens)));
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const Geometry g = geometry(layer->rows, layer->cols);
+    const Plan plan = plan_for(g, tokens, device_cu_count());
+    if (fused_fits(g, tokens, plan)) {
+      const GemmArgs a = layer_args(layer, g, tokens, y, y_dtype, ld_y);
+      const RowsFused f{x, ld_x, int(layer->cols)};
+      if (x_dtype == GPTQ_DT_F32) return launch_rows_waves<float, 1, true>(a, f, plan.waves, s);
+      if (x_dtype == GPTQ_DT_BF16) return launch_rows_waves<bf16_t, 1, true>(a, f, plan.waves, s);
+      return launch_rows_waves<f16_t, 1, true>(a, f, plan.waves, s);
+    }
     char *p = static_cast<char *>(ws);
     int8_t *codes = reinterpret_cast<int8_t *>(p);
     float *scale = reinterpret_cast<float *>(p + codes_bytes(layer, tokens));
     int32_t *sum = reinterpret_cast<int32_t *>(p + codes_bytes(layer, tokens) +
                                                align256(size_t(tokens) * 4));
     void *rest = p + codes_bytes(layer, tokens) + 2 * align256(size_t(tokens) * 4);
-    const hipStream_t s = static_cast<hipStream_t>(stream);
     GPTQ_TRY(quantize_impl(x, nullptr, x_dtype, tokens, layer->cols, ld_x, codes, layer->k_pad,
                            scale, sum, s, "quantize_tokens"));
     return gemm_launch(layer, codes, layer->k_pad, scale, sum, tokens, y, y_dtype, ld_y, rest, s);
