@@ -102,55 +102,83 @@ struct GemmArgs {
 
 // Result blocks of a wave: acc[i][j] holds rows r0 + 16 i + 4 (l / 16) .. + 3
 // (registers) of token t0 + 16 j + l % 16 (l the lane).
+//
+// Stored as they lie, a wave's store would touch 16 tokens' rows for 32 bytes
+// each.  They are turned in the wave's own piece of LDS instead, half the
+// token blocks at a time: token-major rows of 16 FA values, whose 16-byte
+// pieces are XOR-swizzled so that neither side meets bank conflicts; a store
+// then writes 16 FA consecutive values per token.  (Direct stores took 25 us
+// per 256 x 256 tile, as long as 17 of its 128-k stages.)
 template <typename T, int FA, int FB>
 __device__ __forceinline__ void store_typed(const GemmArgs &a, const i32x4_t (&acc)[FA][FB],
-                                            int t0, int r0, int lane) {
-  float st[FB];
-  int sum[FB];
+                                            int t0, int r0, int lane, uint8_t *lds) {
+  constexpr int kRow = 16 * FA * sizeof(T), kPieces = kRow / 16, kHalf = (FB + 1) / 2;
+  constexpr int kVals = 16 / sizeof(T);
+  auto place = [&](int t, int piece) {
+    const int x = kPieces >= 16 ? t & 15 : kPieces == 8 ? (t >> 1) & 7 : (t >> 2) & (kPieces - 1);
+    return lds + t * kRow + ((piece ^ x) << 4);
+  };
+  const int g = lane >> 4;
 #pragma unroll
-  for (int j = 0; j < FB; ++j) {
-    const int t = min(t0 + 16 * j + (lane & 15), a.tokens - 1);
-    st[j] = a.x_scale[t];
-    sum[j] = a.x_sum[t];
-  }
+  for (int j0 = 0; j0 < FB; j0 += kHalf) {
+    float st[kHalf];
+    int sum[kHalf];
 #pragma unroll
-  for (int i = 0; i < FA; ++i) {
-    const int r = r0 + 16 * i + 4 * (lane >> 4), left = a.rows - r;
-    if (left <= 0) continue;
-    // rows_pad is a multiple of 16, so all four are in bounds
-    const f32x4r_t ws = *reinterpret_cast<const f32x4r_t *>(a.w_scale + r);
-    const i32x4_t sh = *reinterpret_cast<const i32x4_t *>(a.w_shift + r);
+    for (int j = 0; j < kHalf; ++j) {
+      const int t = min(t0 + 16 * (j0 + j) + (lane & 15), a.tokens - 1);
+      st[j] = a.x_scale[t];
+      sum[j] = a.x_sum[t];
+    }
 #pragma unroll
-    for (int j = 0; j < FB; ++j) {
-      const int t = t0 + 16 * j + (lane & 15);
-      if (t >= a.tokens) continue;
-      T o[4];
+    for (int i = 0; i < FA; ++i) {
+      const int r = min(r0 + 16 * i, a.row_tiles * 16 - 16) + 4 * g;   // past the layer: unused
+      const f32x4r_t ws = *reinterpret_cast<const f32x4r_t *>(a.w_scale + r);
+      const i32x4_t sh = *reinterpret_cast<const i32x4_t *>(a.w_shift + r);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        float f = float(int(uint32_t(acc[i][j][v]) - uint32_t(sh[v]) * uint32_t(sum[j]))) *
-                  (st[j] * ws[v]);
-        // rounded to float32 before it is narrowed (not in one
-        // mixed-precision multiply)
-        asm("" : "+v"(f));
-        o[v] = narrow<T>(f);
+      for (int j = 0; j < kHalf; ++j) {
+        if (j0 + j >= FB) break;
+        T o[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          // z - 128 and the code sum both fit in 24 bits
+          float f = float(acc[i][j0 + j][v] - __mul24(sh[v], sum[j])) * (st[j] * ws[v]);
+          // rounded to float32 before it is narrowed (not in one
+          // mixed-precision multiply)
+          asm("" : "+v"(f));
+          o[v] = narrow<T>(f);
+        }
+        const int byte = (16 * i + 4 * g) * int(sizeof(T));
+        __builtin_memcpy(__builtin_assume_aligned(place(16 * j + (lane & 15), byte >> 4) + (byte & 15),
+                                                  sizeof(o)), o, sizeof(o));
       }
-      T *p = static_cast<T *>(a.y) + int64_t(t) * a.ld_y + r;
-      if (left >= 4) {
-        __builtin_memcpy(p, o, sizeof(o));
-      } else {
+    }
 #pragma unroll
-        for (int v = 0; v < 3; ++v)
-          if (v < left) p[v] = o[v];
+    for (int it = 0; it < (kHalf * 16 * kPieces + 63) / 64; ++it) {
+      const int at = it * 64 + lane, t = at / kPieces, piece = at % kPieces;
+      if (t >= kHalf * 16) continue;
+      const u32x4r_t v = *reinterpret_cast<const u32x4r_t *>(place(t, piece));
+      const int tok = t0 + 16 * j0 + t, r = r0 + piece * kVals, left = a.rows - r;
+      if (tok >= a.tokens || left <= 0) continue;
+      T *p = static_cast<T *>(a.y) + int64_t(tok) * a.ld_y + r;
+      if (left >= kVals) {
+        __builtin_memcpy(p, &v, 16);
+      } else {
+        T o[kVals];
+        __builtin_memcpy(o, &v, 16);
+#pragma unroll
+        for (int e = 0; e < kVals - 1; ++e)
+          if (e < left) p[e] = o[e];
       }
     }
   }
 }
+// `lds`: the wave's own 16 FA * 16 ceil(FB / 2) * 4 bytes.
 template <int FA, int FB>
 __device__ __forceinline__ void store_blocks(const GemmArgs &a, const i32x4_t (&acc)[FA][FB],
-                                             int t0, int r0, int lane) {
-  if (a.y_type == GPTQ_DT_F32) store_typed<float>(a, acc, t0, r0, lane);
-  else if (a.y_type == GPTQ_DT_BF16) store_typed<bf16_t>(a, acc, t0, r0, lane);
-  else store_typed<f16_t>(a, acc, t0, r0, lane);
+                                             int t0, int r0, int lane, uint8_t *lds) {
+  if (a.y_type == GPTQ_DT_F32) store_typed<float>(a, acc, t0, r0, lane, lds);
+  else if (a.y_type == GPTQ_DT_BF16) store_typed<bf16_t>(a, acc, t0, r0, lane, lds);
+  else store_typed<f16_t>(a, acc, t0, r0, lane, lds);
 }
 
 // A workgroup barrier that orders LDS accesses only: loads from memory stay
@@ -354,7 +382,9 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FA 
       for (int j = 0; j < FB; ++j) p[(i * FB + j) * 64] = acc[i][j];
     return;
   }
-  store_blocks<FA, FB>(a, acc, t0 + wn * 16 * FB, (rt0 + wm * FA) * 16, lane);
+  lds_barrier();                           // every wave is done with the stages
+  store_blocks<FA, FB>(a, acc, t0 + wn * 16 * FB, (rt0 + wm * FA) * 16, lane,
+                       smem + wave * (kStageBytes / 2));
 }
 
 // Adds a split product's parts: a wave per block row (FB blocks) of a tile's
@@ -362,6 +392,8 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FA 
 template <int FA, int FB>
 __global__ void __launch_bounds__(256)
     w8a8_join_kernel(GemmArgs a, int token_tiles, int row_tiles, int splits) {
+  constexpr int kPiece = 16 * 16 * ((FB + 1) / 2) * 4;
+  __shared__ __align__(16) uint8_t lds[4 * kPiece];
   const int lane = threadIdx.x & 63;
   const int unit = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
   const int i = unit % FA, wave = unit / FA % 4, tile = unit / (4 * FA);
@@ -380,7 +412,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int j = 0; j < FB; ++j) acc[0][j] += p[j * 64];
   }
-  store_blocks<1, FB>(a, acc, t0, r0, lane);
+  store_blocks<1, FB>(a, acc, t0, r0, lane, lds + (threadIdx.x >> 6) * kPiece);
 }
 
 // ---- Few tokens: a workgroup per 16 rows, its waves splitting k.  A wave
