@@ -54,44 +54,142 @@ __device__ __forceinline__ f16_t narrow<f16_t>(float v) {
   return f16_t{__builtin_bit_cast(uint16_t, _Float16(v))};
 }
 
-// Eight consecutive elements at p, of which the first n exist (n >= 8: all).
-// The full case is one 16-byte access (two in float32) at the element's own
-// alignment: gfx950 takes global accesses of any alignment, and an aligned
-// row costs nothing for it, so odd widths and strides need no second path.
+// How a row's width d ends, known at launch: in whole groups of 8 elements, in
+// a ragged one, or before the first is full.
+enum Ends { kWhole = 0, kRagged = 1, kShort = 2 };
+inline Ends ends_of(int64_t d) { return d < 8 ? kShort : d % 8 ? kRagged : kWhole; }
+
+// Eight consecutive elements e0 .. e0 + 7 of a row of d, in two steps, so that
+// a lane's loads are all in flight before the first is waited for: fetch8
+// loads without a branch (the row's last eight where e0 + 8 > d), widen8 turns
+// the elements into float32, moves those of a ragged end into place and puts
+// `fill` where there are none.  A fetch is one 16-byte access (two in float32)
+// at the element's own alignment: gfx950 takes global accesses of any
+// alignment, and an aligned row costs nothing for it.
 template <typename T>
 struct Pack8 {
-  T v[8];
+  uint32_t w[2 * sizeof(T)];     // whole words: the load stays one access
+  __device__ __forceinline__ float at(int j) const;
 };
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, int n, float out[8]) {
-  if (n >= 8) {
-    Pack8<T> k;
-    __builtin_memcpy(&k, p, sizeof(k));
-#pragma unroll
-    for (int j = 0; j < 8; ++j) out[j] = widen(k.v[j]);
+template <>
+__device__ __forceinline__ float Pack8<float>::at(int j) const { return __uint_as_float(w[j]); }
+template <>
+__device__ __forceinline__ float Pack8<bf16_t>::at(int j) const {
+  return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+}
+template <>
+__device__ __forceinline__ float Pack8<f16_t>::at(int j) const {
+  return float(__builtin_bit_cast(_Float16, uint16_t(w[j >> 1] >> (16 * (j & 1)))));
+}
+template <Ends E, typename T>
+__device__ __forceinline__ Pack8<T> fetch8(const T *row, int e0, int d) {
+  Pack8<T> k = {};
+  if (E != kShort) {
+    __builtin_memcpy(&k, row + min(e0, d - 8), sizeof(k));
   } else {
+    constexpr int kPerWord = 4 / sizeof(T);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) out[j] = j < n ? widen(p[j]) : 0.f;
+    for (int j = 0; j < 7; ++j)
+      if (j < d) {
+        uint32_t bits = 0;
+        __builtin_memcpy(&bits, row + j, sizeof(T));
+        k.w[j / kPerWord] |= bits << (32 / kPerWord * (j % kPerWord));
+      }
+  }
+  return k;
+}
+// The elements moved down by s places (0..8), zeros following.
+template <typename T>
+__device__ __forceinline__ Pack8<T> move_down(Pack8<T> k, int s) {
+  constexpr int W = 2 * sizeof(T);
+  int words = s;
+  if (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      k.w[i] = __builtin_amdgcn_alignbit(i + 1 < W ? k.w[i + 1] : 0u, k.w[i], (s & 1) * 16);
+    words = s >> 1;
+  }
+#pragma unroll
+  for (int step = 1; step <= W; step *= 2)
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      k.w[i] = words & step ? (i + step < W ? k.w[i + step] : 0u) : k.w[i];
+  return k;
+}
+template <Ends E, typename T>
+__device__ __forceinline__ void widen8(const Pack8<T> &k, int e0, int d, float fill,
+                                       float out[8]) {
+  const int n = d - e0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) out[j] = k.at(j);
+  if (E == kWhole) {                   // all eight or none
+    if (n <= 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) out[j] = fill;
+    }
+    return;
+  }
+  if (__ballot(n < 8)) {               // a branch of the whole wave, rarely taken
+    if (E == kRagged) {
+      const Pack8<T> m = move_down(k, n < 8 ? min(8 - n, 8) : 0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) out[j] = m.at(j);
+    }
+    if (fill != 0.f) {                 // move_down and fetch8 leave zeros
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j >= n) out[j] = fill;
+    } else if (E == kShort && n <= 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) out[j] = 0.f;
+    }
   }
 }
 template <typename T>
 __device__ __forceinline__ void store8(T *p, int n, const float v[8]) {
   if (n >= 8) {
-    Pack8<T> k;
+    T k[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) k.v[j] = narrow<T>(v[j]);
-    __builtin_memcpy(p, &k, sizeof(k));
+    for (int j = 0; j < 8; ++j) k[j] = narrow<T>(v[j]);
+    __builtin_memcpy(p, k, sizeof(k));
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (j < n) p[j] = narrow<T>(v[j]);
   }
 }
-// The same with the type known only at run time (weight vectors).
-__device__ __forceinline__ void load8_any(const void *p, int type, int64_t at, int n, float out[8]) {
-  if (type == GPTQ_DT_F32) load8(static_cast<const float *>(p) + at, n, out);
-  else if (type == GPTQ_DT_BF16) load8(static_cast<const bf16_t *>(p) + at, n, out);
-  else load8(static_cast<const f16_t *>(p) + at, n, out);
+// Eight values of a weight vector, whose type (of WB bytes) is known only at
+// run time: the load first, without a branch on the type, then the widening.
+template <int WB>
+struct WordOf {
+  using type = f16_t;
+};
+template <>
+struct WordOf<4> {
+  using type = float;
+};
+template <int WB>
+struct RawW {
+  uint32_t k[2 * WB];
+};
+template <Ends E, int WB>
+__device__ __forceinline__ RawW<WB> fetch_w(const void *p, int e0, int d) {
+  using T = typename WordOf<WB>::type;
+  const Pack8<T> k = fetch8<E>(static_cast<const T *>(p), e0, d);
+  RawW<WB> r;
+  __builtin_memcpy(r.k, &k, sizeof(r.k));
+  return r;
+}
+template <Ends E, int WB>
+__device__ __forceinline__ void widen_w(const RawW<WB> &r, int type, int e0, int d, float out[8]) {
+  auto go = [&](auto tag) {
+    Pack8<decltype(tag)> k;
+    __builtin_memcpy(&k, r.k, sizeof(k));
+    widen8<E>(k, e0, d, 0.f, out);
+  };
+  if constexpr (WB == 4) go(float{});
+  else if (type == GPTQ_DT_BF16) go(bf16_t{});
+  else go(f16_t{});
 }
 
 // ------------------------------------------------------------- reductions

@@ -1,11 +1,12 @@
 // Log probabilities of given tokens, entropy and top alternatives from rows
 // of logits, in one pass over the logits.
 //
-// Every lane keeps a running maximum m of its logits, s = sum e^(z - m) and
-// t = sum (z - m) e^(z - m) (in powers of two); lanes, waves and, when a row
-// is split over workgroups, parts are joined by rescaling to the common
-// maximum.  Then ln p = scale (l - m) - ln s and the entropy is
-// ln s - t / s.
+// With c = scale log2 e, every lane keeps a running maximum m of its logits,
+// s = sum 2^(c l - M) and t = sum (c l - M) 2^(c l - M), M being the float
+// nearest c m; lanes, waves and, when a row is split over workgroups, parts
+// are joined by rescaling to the common maximum.  Then ln p = ln 2 (c l - M) -
+// ln s and the entropy is ln s - ln 2 t / s.  c l - M is one fused operation,
+// exact up to its last rounding because M, not c m, is the reference.
 //
 // Alternatives: each wave keeps a short list of candidates in LDS, every
 // logit above a threshold that k logits of the wave are known to reach.  The
@@ -24,7 +25,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kChunkElems = 8 * kThreads;   // elements a workgroup takes per chunk
-constexpr int kUnroll = 4;                  // chunks per tile
 constexpr int kMaxTop = 64;
 // A wave's list takes a whole chunk (512) on top of k cut entries.
 constexpr int kListCap = 512 + kMaxTop;
@@ -44,6 +44,8 @@ struct ScoreArgs {
   uint64_t *part_keys;          //             and k keys
 };
 constexpr int kPartWords = 4;   // m, s, t, rank count
+
+constexpr float kLog2e = 1.4426950408889634f;
 
 // Floats as integers of the same order; -0 and +0 are equal.
 __device__ __forceinline__ uint32_t ordered(float v) {
@@ -65,14 +67,30 @@ __device__ __forceinline__ uint64_t make_key(float v, int index) {
 __device__ __forceinline__ float key_value(uint64_t key) { return from_ordered(uint32_t(key >> 32)); }
 __device__ __forceinline__ int key_index(uint64_t key) { return int(~uint32_t(key)); }
 
+// c l - M for a row maximum m.  Where c m is too large for that (a row of
+// masks at the type's lowest value), c (l - m), halved against overflow.
+constexpr float kLarge = 1e30f;
+// M: the product rounded, never fused into what uses it.
+__device__ __forceinline__ float reference(float m, float c) {
+  float M = m * c;
+  asm("" : "+v"(M));
+  return M;
+}
+__device__ __forceinline__ float exponent(float l, float m, float c) {
+  const float M = reference(m, c);
+  return fabsf(M) < kLarge ? __builtin_fmaf(l, c, -M) : (0.5f * l - 0.5f * m) * c * 2.f;
+}
+
 // Running softmax statistics of part of a row; empty: s = 0.
 struct Stat {
   float m, s, t;
 };
-// Joins b into a; c2 = scale log2 e.
-__device__ __forceinline__ void join(Stat &a, const Stat &b, float c2) {
-  const float m = fmaxf(a.m, b.m);
-  const float da = (a.m - m) * c2, db = (b.m - m) * c2;
+// Joins b into a.
+__device__ __forceinline__ void join(Stat &a, const Stat &b, float c) {
+  const float m = fmaxf(a.m, b.m), M = reference(m, c);
+  const bool plain = fabsf(M) < kLarge;
+  const float da = plain ? reference(a.m, c) - M : exponent(a.m, m, c);
+  const float db = plain ? reference(b.m, c) - M : exponent(b.m, m, c);
   const float fa = exp2f(da), fb = exp2f(db);
   // a part scaled to nothing adds nothing (its t would be 0 * infinity)
   const float ta = fa > 0.f ? fa * (a.t + da * a.s) : 0.f;
@@ -80,51 +98,88 @@ __device__ __forceinline__ void join(Stat &a, const Stat &b, float c2) {
   a = Stat{m, fa * a.s + fb * b.s, ta + tb};
 }
 
+// Joins the lanes' statistics, in a fixed order.
+__device__ __forceinline__ void join_wave(Stat &st, float c) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const Stat o{__shfl_xor(st.m, m), __shfl_xor(st.s, m), __shfl_xor(st.t, m)};
+    // same operand order on both sides, so both get the same bits
+    Stat lo = lane & m ? o : st;
+    join(lo, lane & m ? st : o, c);
+    st = lo;
+  }
+}
+
 // Cuts the list of n keys to its k best, exactly (k < n <= kListCap), and
-// returns the smallest kept value.  Two searches by counting: the k-th
-// largest value bit by bit, then, if more than k reach it, the highest index
-// to keep among those equal to it.  One wave; the list is in its LDS.
+// returns the smallest kept value.  The k-th largest value is searched bit by
+// bit, counting with ballots, from the first bit that differs within the list;
+// if more than k entries reach it, their lowest indices are searched the same
+// way.  One wave; the list is in its LDS.
 __device__ __forceinline__ float cut_list(uint64_t *list, int n, int k) {
   constexpr int kPer = kListCap / 64;   // 9
   const int lane = threadIdx.x & 63;
-  uint64_t e[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) e[i] = lane + 64 * i < n ? list[lane + 64 * i] : 0;
-  const int used = (n + 63) / 64;
-  auto count_at_least = [&](uint64_t key) {
-    int c = 0;
-    for (int i = 0; i < kPer; ++i)
-      if (i < used) c += __popcll(__ballot(e[i] >= key));
-    return c;
-  };
-  // the largest key that k entries reach (keys are distinct, so exactly k)
-  uint64_t key = 0;
-  for (int bit = 63; bit >= 0; --bit) {
-    const uint64_t probe = key | (uint64_t(1) << bit);
-    const int c = count_at_least(probe);
-    if (c >= k) key = probe;
-    if (c == k) break;
-  }
-  int at = 0;
+  uint32_t hi[kPer], lo[kPer];
+  uint32_t any = 0, all = ~0u;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const bool keep = e[i] >= key && e[i] != 0;
+    const uint64_t e = lane + 64 * i < n ? list[lane + 64 * i] : 0;
+    hi[i] = uint32_t(e >> 32);
+    lo[i] = uint32_t(e);
+    if (lane + 64 * i < n) any |= hi[i], all &= hi[i];
+  }
+  const int used = (n + 63) / 64;
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) {
+    any |= uint32_t(__shfl_xor(int(any), m));
+    all &= uint32_t(__shfl_xor(int(all), m));
+  }
+  const uint32_t spread = __builtin_amdgcn_readfirstlane(any ^ all);
+  uint32_t value = __builtin_amdgcn_readfirstlane(all) &
+                   (spread ? ~((2u << (31 - __builtin_clz(spread))) - 1) : ~0u);
+  int reach = n;                        // entries >= value
+  for (int bit = spread ? 31 - __builtin_clz(spread) : -1; bit >= 0 && reach > k; --bit) {
+    const uint32_t probe = value | (1u << bit);
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < used) c += __popcll(__ballot(hi[i] >= probe));
+    if (c >= k) value = probe, reach = c;
+  }
+  uint32_t low = 0;                     // of those equal to value: keep lo >= low
+  if (reach > k) {
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t probe = low | (1u << bit);
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (i < used) c += __popcll(__ballot(hi[i] > value || (hi[i] == value && lo[i] >= probe)));
+      if (c >= k) low = probe;
+      if (c == k) break;
+    }
+  }
+  int at = 0;
+  uint32_t least = ~0u;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (i >= used) break;
+    const bool keep = hi[i] > value || (hi[i] == value && lo[i] >= low && lane + 64 * i < n);
     const uint64_t mask = __ballot(keep);
-    if (keep) list[at + __popcll(mask & ((uint64_t(1) << lane) - 1))] = e[i];
+    if (keep) {
+      list[at + __popcll(mask & ((uint64_t(1) << lane) - 1))] = (uint64_t(hi[i]) << 32) | lo[i];
+      least = min(least, hi[i]);
+    }
     at += __popcll(mask);
   }
-  // the k kept keys now lie in the first k places; their smallest value
-  uint64_t least = ~uint64_t(0);
-  __builtin_amdgcn_wave_barrier();
-  if (lane < k) least = list[lane];
-  uint32_t hi = uint32_t(least >> 32);
 #pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) hi = min(hi, uint32_t(__shfl_xor(int(hi), m)));
-  return from_ordered(hi);
+  for (int m = 32; m >= 1; m >>= 1) least = min(least, uint32_t(__shfl_xor(int(least), m)));
+  return from_ordered(least);
 }
 
 // First tile: a value that at least k of the wave's elements reach, the k-th
-// largest of its 256 chunk maxima or a little below (-inf if fewer are above).
+// largest of its maxima over 8 elements or a little below (-inf if fewer than
+// k are above).
+template <int kUnroll>
 __device__ __forceinline__ float first_threshold(const float cmax[kUnroll], int k) {
   uint32_t o[kUnroll];
 #pragma unroll
@@ -142,18 +197,19 @@ __device__ __forceinline__ float first_threshold(const float cmax[kUnroll], int 
   return f > -INFINITY ? f : -INFINITY;    // also for patterns below -inf
 }
 
-// scale (l - m); halves, so that the difference of two large floats stays
-// finite where its product with the scale is.
-__device__ __forceinline__ float scaled_difference(float l, float m, float scale) {
-  return (0.5f * l - 0.5f * m) * scale * 2.f;
-}
-
 // The final outputs of a row from its joined statistics.
+constexpr float kLn2 = 0.6931471805599453f;
 struct RowOut {
-  float m, log_s, entropy, logprob;
+  float m, c, log_s, entropy, logprob;
   int rank;
   bool bad, empty;
 };
+// ln p of an entry of value l (not of an empty row).
+__device__ __forceinline__ float log_prob(const ScoreArgs &a, const RowOut &o, float l) {
+  const bool plain = fabsf(o.m * o.c) < kLarge && fabsf(l * o.c) < kLarge;
+  const float d = plain ? kLn2 * exponent(l, o.m, o.c) : (0.5f * l - 0.5f * o.m) * a.scale * 2.f;
+  return d - o.log_s;
+}
 __device__ __forceinline__ RowOut finish_row(const ScoreArgs &a, const Stat &st, int rank_count,
                                              int64_t id, float given) {
   RowOut o;
@@ -161,10 +217,11 @@ __device__ __forceinline__ RowOut finish_row(const ScoreArgs &a, const Stat &st,
   o.bad = !(st.s >= 0.f) || st.m == INFINITY;     // NaN or +inf somewhere
   o.empty = st.s == 0.f;
   o.m = st.m;
+  o.c = a.scale * kLog2e;
   o.log_s = logf(st.s);
-  o.entropy = o.bad ? nan : o.empty ? 0.f : o.log_s - 0.6931471805599453f * (st.t / st.s);
+  o.entropy = o.bad ? nan : o.empty ? 0.f : o.log_s - kLn2 * (st.t / st.s);
   o.rank = rank_count;
-  o.logprob = o.empty ? -INFINITY : scaled_difference(given, o.m, a.scale) - o.log_s;
+  o.logprob = o.empty ? -INFINITY : log_prob(a, o, given);
   if (o.bad) o.logprob = nan, o.rank = -1;
   if (id >= a.vocab) o.logprob = nan, o.rank = -1;
   if (id < 0) o.logprob = o.bad ? nan : 0.f, o.rank = -1;
@@ -183,7 +240,7 @@ __device__ __forceinline__ void write_top(const ScoreArgs &a, int64_t row, int p
   const float nan = __uint_as_float(0x7fc00000u);
   a.top_ids[row * a.k + p] = o.bad || !present ? -1 : key_index(key);
   a.top_logprobs[row * a.k + p] =
-      o.bad ? nan : present ? scaled_difference(key_value(key), o.m, a.scale) - o.log_s : -INFINITY;
+      o.bad ? nan : present ? log_prob(a, o, key_value(key)) : -INFINITY;
 }
 
 __device__ __forceinline__ float load_one(const float *p) { return *p; }
@@ -191,7 +248,7 @@ __device__ __forceinline__ float load_one(const bf16_t *p) { return widen(*p); }
 __device__ __forceinline__ float load_one(const f16_t *p) { return widen(*p); }
 
 // Workgroup (row, split): the row's elements [split seg, split seg + seg).
-template <typename T, bool TOP>
+template <typename T, Ends E, int kUnroll, bool TOP>
 __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
   __shared__ uint64_t lists[TOP ? kWaves * kListCap : 1];
   __shared__ Stat slot[kWaves];
@@ -202,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const T *l = static_cast<const T *>(a.logits) + row * a.ld;
   const int v0 = split * a.seg, v1 = min(v0 + a.seg, a.vocab);
-  const float c2 = a.scale * 1.4426950408889634f;
+  const float c = a.scale * kLog2e;
 
   const int64_t id = a.ids ? a.ids[row] : -1;
   const bool given = id >= 0 && id < a.vocab;
@@ -211,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
   const float lt_below = lt > -INFINITY ? below(lt) : INFINITY;
 
   Stat st{-3.402823466e38f, 0.f, 0.f};
-  int ahead = 0;
+  int ahead = 0;                   // the wave's count
   uint64_t *list = lists + (TOP ? wave * kListCap : 0);
   int n = 0;                       // list length (wave-uniform)
   float thr = -INFINITY;           // candidates are > thr
@@ -219,68 +276,82 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
 
   for (int tile = v0; tile < v1; tile += kUnroll * kChunkElems) {
     float x[kUnroll][8], cmax[kUnroll];
+    Pack8<T> raw[kUnroll];
 #pragma unroll
-    for (int c = 0; c < kUnroll; ++c) {
-      const int e0 = tile + c * kChunkElems + 8 * tid, left = v1 - e0;
-      load8(l + min(e0, a.vocab - 1), left, x[c]);
-      if (left < 8) {
+    for (int q = 0; q < kUnroll; ++q) raw[q] = fetch8<E>(l, tile + q * kChunkElems + 8 * tid, v1);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j >= left) x[c][j] = -INFINITY;
-      }
-    }
+    for (int q = 0; q < kUnroll; ++q)
+      widen8<E>(raw[q], tile + q * kChunkElems + 8 * tid, v1, -INFINITY, x[q]);
     float m = st.m;
 #pragma unroll
-    for (int c = 0; c < kUnroll; ++c) {
-      cmax[c] = x[c][0];
+    for (int q = 0; q < kUnroll; ++q) {
+      cmax[q] = x[q][0];
 #pragma unroll
-      for (int j = 1; j < 8; ++j) cmax[c] = fmaxf(cmax[c], x[c][j]);
-      m = fmaxf(m, cmax[c]);
+      for (int j = 1; j < 8; ++j) cmax[q] = fmaxf(cmax[q], x[q][j]);
+      m = fmaxf(m, cmax[q]);
     }
-    if (m > st.m) {                // rescale to the new maximum
-      const float dm = (st.m - m) * c2, f = __builtin_amdgcn_exp2f(dm);
+    const float M = reference(m, c);
+    if (!__ballot(!(fabsf(M) < kLarge))) {
+      // (a lane whose elements were all -infinity so far has s = t = 0)
+      const float dm = fmaxf(reference(st.m, c) - M, -200.f), f = __builtin_amdgcn_exp2f(dm);
+      st.t = f * (st.t + dm * st.s);
+      st.s *= f;
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float d = __builtin_fmaf(x[i][j], c, -M);
+          const float e = __builtin_amdgcn_exp2f(d);
+          st.s += e;
+          st.t = __builtin_fmaf(fmaxf(d, -3e38f), e, st.t);   // -inf: 0
+        }
+    } else {
+      // Some lane has only -infinity or huge values so far.
+      const float dm = exponent(st.m, m, c), f = exp2f(dm);
       st.t = f > 0.f ? f * (st.t + dm * st.s) : 0.f;
       st.s *= f;
-      st.m = m;
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float d = exponent(x[i][j], m, c), e = exp2f(d);
+          st.s += e;
+          st.t += fmaxf(d, -3e38f) * e;
+        }
     }
-#pragma unroll
-    for (int c = 0; c < kUnroll; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float d = (x[c][j] - m) * c2;
-        const float e = __builtin_amdgcn_exp2f(d);
-        st.s += e;
-        st.t += fmaxf(d, -3e38f) * e;   // -inf: 0
-      }
+    st.m = m;
     if (given) {
 #pragma unroll
-      for (int c = 0; c < kUnroll; ++c) {
+      for (int q = 0; q < kUnroll; ++q) {
         // Entries before the given token count from its value up, entries
         // after it from above its value.
-        const int e0 = tile + c * kChunkElems + 8 * tid;
+        const int e0 = tile + q * kChunkElems + 8 * tid;
         const bool before = e0 + 7 < at;
         const float from = before ? lt_below : lt;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ahead += x[c][j] > from;
-        if (before && e0 < v1 && lt == -INFINITY) ahead += 8;   // all of them: >= -inf
-        if (!before && e0 < at && e0 < v1) {
+        for (int j = 0; j < 8; ++j) ahead += __popcll(__ballot(x[q][j] > from));
+        const bool has_given = !before && e0 < at && e0 < v1;
+        const bool masked = before && e0 < v1 && lt == -INFINITY;   // all eight are >= -inf
+        if (__ballot(has_given || masked)) {
+          ahead += 8 * __popcll(__ballot(masked));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ahead += (e0 + j < at) && x[c][j] == lt;
+          for (int j = 0; j < 8; ++j)
+            ahead += __popcll(__ballot(has_given && e0 + j < at && x[q][j] == lt));
         }
       }
     }
     if (TOP) {
       float strict = thr;
       if (tile == v0) {
-        strict = first_threshold(cmax, a.k);
+        strict = first_threshold<kUnroll>(cmax, a.k);
         if (strict > -INFINITY) thr = below(strict);
       }
 #pragma unroll
-      for (int c = 0; c < kUnroll; ++c) {
-        if (!__ballot(cmax[c] > thr)) continue;
+      for (int q = 0; q < kUnroll; ++q) {
+        if (!__ballot(cmax[q] > thr)) continue;
         int add = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) add += __popcll(__ballot(x[c][j] > thr));
+        for (int j = 0; j < 8; ++j) add += __popcll(__ballot(x[q][j] > thr));
         if (n + add > kListCap) {      // wave-uniform; then n is k and a chunk fits
           strict = cut_list(list, n, a.k);
           thr = fmaxf(thr, strict);
@@ -288,11 +359,11 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const bool take = x[c][j] > thr;
+          const bool take = x[q][j] > thr;
           const uint64_t mask = __ballot(take);
           if (take)
             list[n + __popcll(mask & ((uint64_t(1) << lane) - 1))] =
-                make_key(x[c][j], tile + c * kChunkElems + 8 * tid + j);
+                make_key(x[q][j], tile + q * kChunkElems + 8 * tid + j);
           n += __popcll(mask);
         }
       }
@@ -306,16 +377,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
     }
   }
 
-  // Join the lanes, then the waves, in a fixed order.
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const Stat o{__shfl_xor(st.m, m), __shfl_xor(st.s, m), __shfl_xor(st.t, m)};
-    // same operand order on both sides, so both get the same bits
-    Stat lo = lane & m ? o : st;
-    join(lo, lane & m ? st : o, c2);
-    st = lo;
-  }
-  ahead = wave_all<SumI>(ahead);
+  join_wave(st, c);
   if (TOP && n > a.k) {
     cut_list(list, n, a.k);
     n = a.k;
@@ -330,7 +392,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
   ahead = slot_rank[0];
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) {
-    join(st, slot[w], c2);
+    join(st, slot[w], c);
     ahead += slot_rank[w];
   }
   const bool whole = a.splits == 1;
@@ -367,73 +429,60 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
   }
 }
 
-// Joins a row's splits: one workgroup per row.  More keys than kDirect are
-// first cut to the k best by the same search as a wave's list (the largest
-// key that k entries reach), over the workgroup.
-constexpr int kDirect = 256;
+// Joins a row's splits: one workgroup per row.  The splits' lists are sorted,
+// so with p = ceil(k / splits) the least of their p-th keys is one that k keys
+// reach; only keys from there on are ranked against each other.
+constexpr int kMaxJoin = 1024;   // splits * k
 constexpr int kMaxSplits = 64;
 template <typename T>
 __global__ void __launch_bounds__(kThreads) score_join_kernel(ScoreArgs a) {
-  __shared__ uint64_t keys[kDirect];
-  __shared__ int counts[2][kWaves], kept;
-  constexpr int kPer = kMaxSplits * kMaxTop / kThreads;   // 16
+  __shared__ uint64_t keys[kMaxJoin];
+  __shared__ uint64_t bound;
+  __shared__ int kept;
   const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x, wave = tid >> 6;
-  const float c2 = a.scale * 1.4426950408889634f;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const float c = a.scale * kLog2e;
+  const int n = a.splits * a.k;
+  const uint64_t *src = a.part_keys + row * n;
+  uint64_t mine[kMaxJoin / kThreads];
+#pragma unroll
+  for (int i = 0; i < kMaxJoin / kThreads; ++i)
+    mine[i] = tid + kThreads * i < n ? src[tid + kThreads * i] : 0;
+  // the splits' statistics, one lane each, joined over the wave
+  const float *p = a.part + row * a.splits * kPartWords + min(lane, a.splits - 1) * kPartWords;
   const int64_t id = a.ids ? a.ids[row] : -1;
   const bool given = id >= 0 && id < a.vocab;
   const float lt = given ? load_one(static_cast<const T *>(a.logits) + row * a.ld + id) : 0.f;
-  const float *p = a.part + row * a.splits * kPartWords;
   Stat st{p[0], p[1], p[2]};
   int ahead = __float_as_int(p[3]);
-  for (int s = 1; s < a.splits; ++s) {
-    const float *q = p + s * kPartWords;
-    join(st, Stat{q[0], q[1], q[2]}, c2);
-    ahead += __float_as_int(q[3]);
-  }
+  if (lane >= a.splits) st = Stat{-3.402823466e38f, 0.f, 0.f}, ahead = 0;
+  join_wave(st, c);
+  ahead = wave_all<SumI>(ahead);
   const RowOut o = finish_row(a, st, ahead, id, lt);
   if (tid == 0) write_scalars(a, row, o);
   if (a.k == 0) return;
-  int n = a.splits * a.k;
-  const uint64_t *src = a.part_keys + row * n;
-  if (n <= kDirect) {
-    keys[tid] = tid < n ? src[tid] : 0;
-  } else {
-    uint64_t e[kPer];
+  if (tid < 64) {
+    uint64_t key = lane < a.splits ? src[lane * a.k + (a.k + a.splits - 1) / a.splits - 1]
+                                   : ~uint64_t(0);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) e[i] = tid + kThreads * i < n ? src[tid + kThreads * i] : 0;
-    if (tid == 0) kept = 0;
-    uint64_t key = 0;
-    for (int bit = 63; bit >= 0; --bit) {
-      const uint64_t probe = key | (uint64_t(1) << bit);
-      int c = 0;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (kThreads * i < n) c += __popcll(__ballot(e[i] >= probe));
-      if ((tid & 63) == 0) counts[bit & 1][wave] = c;
-      __syncthreads();
-      c = 0;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) c += counts[bit & 1][w];
-      if (c >= a.k) key = probe;
-      if (c == a.k) break;
+    for (int m = 32; m >= 1; m >>= 1) {
+      const uint64_t other = __shfl_xor(static_cast<unsigned long long>(key), m);
+      key = other < key ? other : key;
     }
-    keys[tid] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (e[i] != 0 && e[i] >= key)      // at most k of them, in any order
-        keys[atomicAdd(&kept, 1)] = e[i];
-    n = a.k;
+    if (tid == 0) bound = key, kept = 0;
   }
   __syncthreads();
-  const uint64_t key = tid < n ? keys[tid] : 0;
-  int place = 0, total = 0;
-  for (int i = 0; i < n; ++i) {
-    place += keys[i] > key;
-    total += keys[i] != 0;
+#pragma unroll
+  for (int i = 0; i < kMaxJoin / kThreads; ++i)
+    if (mine[i] != 0 && mine[i] >= bound) keys[atomicAdd(&kept, 1)] = mine[i];   // in any order
+  __syncthreads();
+  const int total = kept;
+  for (int at = tid; at < total; at += kThreads) {
+    const uint64_t key = keys[at];
+    int place = 0;
+    for (int i = 0; i < total; ++i) place += keys[i] > key;
+    if (place < a.k) write_top(a, row, place, o, true, key);
   }
-  if (key != 0 && place < a.k) write_top(a, row, place, o, true, key);
   if (tid >= total && tid < a.k) write_top(a, row, tid, o, false, 0);
 }
 
@@ -442,27 +491,43 @@ __global__ void __launch_bounds__(kThreads) score_join_kernel(ScoreArgs a) {
 struct ScorePlan {
   int splits, seg;
 };
-ScorePlan score_plan(int64_t rows, int64_t vocab, int cus) {
+ScorePlan score_plan(int64_t rows, int64_t vocab, int32_t k, int cus) {
   const int64_t chunks = cdiv(vocab, kChunkElems);
-  const int64_t want = std::min<int64_t>(chunks, cdiv(4 * int64_t(cus), rows));
-  const int64_t per = cdiv(chunks, std::min<int64_t>(want, kMaxSplits));
+  const int64_t most = std::min<int64_t>(kMaxSplits, kMaxJoin / std::max(k, 1));
+  const int64_t want = std::min<int64_t>({chunks, cdiv(4 * int64_t(cus), rows), most});
+  const int64_t per = cdiv(chunks, want);
   return {int(cdiv(chunks, per)), int(per * kChunkElems)};
 }
 
 constexpr size_t kPartBytes = kPartWords * sizeof(float);
 
 size_t score_ws(int64_t rows, int64_t vocab, int32_t k, int cus) {
-  const ScorePlan p = score_plan(rows, vocab, cus);
+  const ScorePlan p = score_plan(rows, vocab, k, cus);
   if (p.splits == 1) return 0;
   return align256(size_t(rows) * p.splits * kPartBytes) +
          align256(size_t(rows) * p.splits * size_t(k) * sizeof(uint64_t));
 }
 
+// One chunk per tile where a workgroup has few of them (single tokens), four
+// otherwise, whose loads are then in flight together.
+template <typename T, Ends E, int kUnroll>
+gptq_status score_tiles(const ScoreArgs &a, int64_t rows, hipStream_t s) {
+  const dim3 grid(uint32_t(rows * a.splits)), block(kThreads);
+  return a.k ? launch("token_logprobs", score_kernel<T, E, kUnroll, true>, grid, block, 0, s, a)
+             : launch("token_logprobs", score_kernel<T, E, kUnroll, false>, grid, block, 0, s, a);
+}
+template <typename T, Ends E>
+gptq_status score_ends(const ScoreArgs &a, int64_t rows, hipStream_t s) {
+  return a.seg <= 2 * kChunkElems ? score_tiles<T, E, 1>(a, rows, s)
+                                  : score_tiles<T, E, 4>(a, rows, s);
+}
 template <typename T>
 gptq_status score_typed(const ScoreArgs &a, int64_t rows, hipStream_t s) {
-  const dim3 grid(uint32_t(rows * a.splits));
-  GPTQ_TRY(a.k ? launch("token_logprobs", score_kernel<T, true>, grid, dim3(kThreads), 0, s, a)
-               : launch("token_logprobs", score_kernel<T, false>, grid, dim3(kThreads), 0, s, a));
+  switch (ends_of(a.vocab)) {
+    case kWhole: GPTQ_TRY((score_ends<T, kWhole>(a, rows, s))); break;
+    case kRagged: GPTQ_TRY((score_ends<T, kRagged>(a, rows, s))); break;
+    default: GPTQ_TRY((score_ends<T, kShort>(a, rows, s)));
+  }
   if (a.splits == 1) return GPTQ_OK;
   return launch("token_logprobs_join", score_join_kernel<T>, dim3(uint32_t(rows)), dim3(kThreads), 0,
                 s, a);
@@ -511,7 +576,7 @@ gptq_status gptq_token_logprobs(const void *logits, int32_t dtype, int64_t rows,
                           (const void *)top_ids, (const void *)top_logprobs})
       if (!aligned_to(p, 4)) return fail(GPTQ_ERR_INVALID_ARG, "outputs must be 4-byte aligned");
     const int cus = device_cu_count();
-    const ScorePlan plan = score_plan(rows, vocab, cus);
+    const ScorePlan plan = score_plan(rows, vocab, top_k, cus);
     const size_t need = score_ws(rows, vocab, top_k, cus);
     if (need) {
       if (!ws) return fail(GPTQ_ERR_WORKSPACE, "workspace is NULL");

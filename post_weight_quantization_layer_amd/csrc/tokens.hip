@@ -48,6 +48,17 @@ __device__ __forceinline__ void store_codes(const float v[NCH][8], int lane, int
   }
 }
 
+// g / (1 + e^-g) within about 6 ulp: e^-g as a power of two whose argument's
+// rounding error is put back (it would be |g| ulp), and a reciprocal instead of
+// a division; at -infinity and +infinity the quotient's own limits.
+__device__ __forceinline__ float silu(float g) {
+  const float t = g * -1.4426950408889634f;
+  const float lo = __builtin_fmaf(g, -1.4426950408889634f, -t) - g * 1.9259629911266175e-8f;
+  const float e = __builtin_amdgcn_exp2f(t);
+  const float r = g * __builtin_amdgcn_rcpf(1.f + __builtin_fmaf(e, lo * 0.6931471805599453f, e));
+  return fabsf(t) < 120.f ? r : g > 0.f ? g : g / (1.f + expf(-g));
+}
+
 struct CodesOut {
   int8_t *codes;
   int64_t ld;      // bytes between rows
@@ -57,7 +68,7 @@ struct CodesOut {
 };
 
 // One row's values: x, or silu(g) u.
-template <typename T, int WPR, int NCH, bool GATED>
+template <typename T, Ends E, int WPR, int NCH, bool GATED>
 __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR)
     quantize_kernel(const T *__restrict__ x, const T *__restrict__ u, int64_t tokens, int cols,
                     int64_t ld, CodesOut out) {
@@ -67,30 +78,31 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR)
   const int lane = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
   const int64_t t = int64_t(blockIdx.x) * kRows + (WPR == 1 ? threadIdx.x >> 6 : 0);
   if (t >= tokens) return;       // whole waves; no barrier when WPR == 1
+  const T *xr = x + t * ld, *ur = GATED ? u + t * ld : nullptr;
+  Pack8<T> kx[NCH], ku[GATED ? NCH : 1];
+#pragma unroll
+  for (int c = 0; c < NCH; ++c) {
+    kx[c] = fetch8<E>(xr, 8 * (c * 64 * WPR + lane), cols);
+    if (GATED) ku[GATED ? c : 0] = fetch8<E>(ur, 8 * (c * 64 * WPR + lane), cols);
+  }
   float v[NCH][8];
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
     const int e0 = 8 * (c * 64 * WPR + lane);
-    load8(x + t * ld + min(e0, cols - 1), cols - e0, v[c]);
-  }
-  if (GATED) {
-    float w[NCH][8];
+    widen8<E>(kx[c], e0, cols, 0.f, v[c]);
+    if (GATED && e0 < cols) {
+      float w[8];
+      widen8<E>(ku[GATED ? c : 0], e0, cols, 0.f, w);
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int e0 = 8 * (c * 64 * WPR + lane);
-      load8(u + t * ld + min(e0, cols - 1), cols - e0, w[c]);
+      for (int j = 0; j < 8; ++j) v[c][j] = silu(v[c][j]) * w[j];
     }
-#pragma unroll
-    for (int c = 0; c < NCH; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[c][j] = v[c][j] / (1.f + expf(-v[c][j])) * w[c][j];
   }
   store_codes<WPR, NCH>(v, lane, out.pad, out.codes + t * out.ld, out.scale + t, out.sum + t,
                         slot_max, slot_sum);
 }
 
 // Rows wider than 64 * 16 * 4 * 8 = 32768: two passes over the row.
-template <typename T, bool GATED>
+template <typename T, Ends E, bool GATED>
 __global__ void __launch_bounds__(1024)
     quantize_wide_kernel(const T *__restrict__ x, const T *__restrict__ u, int64_t tokens,
                          int cols, int64_t ld, CodesOut out) {
@@ -99,12 +111,18 @@ __global__ void __launch_bounds__(1024)
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x;
   auto value = [&](int e0, float v[8]) {
-    load8(x + t * ld + min(e0, cols - 1), cols - e0, v);
+    const T *xr = x + t * ld;
+    const Pack8<T> k = fetch8<E>(xr, e0, cols);
     if (GATED) {
+      const T *ur = u + t * ld;
+      const Pack8<T> ku = fetch8<E>(ur, e0, cols);
       float w[8];
-      load8(u + t * ld + min(e0, cols - 1), cols - e0, w);
+      widen8<E>(k, e0, cols, 0.f, v);
+      widen8<E>(ku, e0, cols, 0.f, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = v[j] / (1.f + expf(-v[j])) * w[j];
+      for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * w[j];
+    } else {
+      widen8<E>(k, e0, cols, 0.f, v);
     }
   };
   uint32_t m = 0;
@@ -144,12 +162,29 @@ struct NormArgs {
   CodesOut out;    // codes NULL: none
 };
 
+// The weights of one norm, fetched ahead of their use (four chunks per lane
+// have no registers for that: they are fetched where they are used).
+template <Ends E, int WB, int WPR, int NCH>
+struct NormWeights {
+  RawW<WB> w[NCH], b[NCH];
+  __device__ __forceinline__ void fetch(const void *weight, const void *bias, int d, int lane) {
+    if (NCH == 4) return;
+    if (weight)
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) w[c] = fetch_w<E, WB>(weight, 8 * (c * 64 * WPR + lane), d);
+    if (bias)
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) b[c] = fetch_w<E, WB>(bias, 8 * (c * 64 * WPR + lane), d);
+  }
+};
+
 // v := N(v) with the sums over the row's d elements; chunks past the row
-// stay 0.  Returns nothing for NONE.
-template <int WPR, int NCH>
-__device__ __forceinline__ void normalize(float v[NCH][8], int kind, const void *w, const void *bias,
-                                          int w_type, float offset, float eps, int d, int lane,
-                                          float *slot_mean, float *slot_sq) {
+// stay 0.
+template <Ends E, int WB, int WPR, int NCH>
+__device__ __forceinline__ void normalize(float v[NCH][8], int kind,
+                                          const NormWeights<E, WB, WPR, NCH> &nw, const void *w,
+                                          const void *bias, int w_type, float offset, float eps,
+                                          int d, int lane, float *slot_mean, float *slot_sq) {
   if (kind == GPTQ_NORM_NONE) return;
   if (kind == GPTQ_NORM_LAYER) {
     float s = 0.f;
@@ -173,11 +208,10 @@ __device__ __forceinline__ void normalize(float v[NCH][8], int kind, const void 
   const float rstd = 1.f / sqrtf(row_all<SumF, WPR>(sq, slot_sq) / float(d) + eps);
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int e0 = 8 * (c * 64 * WPR + lane), n = d - e0, at = min(e0, d - 1);
-    if (n <= 0) continue;
+    const int e0 = 8 * (c * 64 * WPR + lane);
     float f[8];
     if (w) {
-      load8_any(w, w_type, at, n, f);
+      widen_w<E, WB>(NCH == 4 ? fetch_w<E, WB>(w, e0, d) : nw.w[c], w_type, e0, d, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[c][j] *= rstd * (offset + f[j]);
     } else {
@@ -185,14 +219,18 @@ __device__ __forceinline__ void normalize(float v[NCH][8], int kind, const void 
       for (int j = 0; j < 8; ++j) v[c][j] *= rstd;
     }
     if (bias) {
-      load8_any(bias, w_type, at, n, f);
+      widen_w<E, WB>(NCH == 4 ? fetch_w<E, WB>(bias, e0, d) : nw.b[c], w_type, e0, d, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[c][j] += f[j];
     }
   }
 }
 
-template <typename T, int WPR, int NCH>
+// One launch for the four passes over the row that the formula names (mean and
+// square of b, of r'): the row stays in registers.  Every vector is fetched
+// before the reduction that its use waits for; with one chunk per lane (few
+// rows) all of them at the start.
+template <typename T, Ends E, int WB, int WPR, int NCH>
 __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) norm_block_kernel(NormArgs a) {
   __shared__ float slots[4][WPR];
   __shared__ uint32_t slot_max[WPR];
@@ -202,43 +240,58 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) norm_block_kernel(N
   const int64_t t = int64_t(blockIdx.x) * kRows + (WPR == 1 ? threadIdx.x >> 6 : 0);
   if (t >= a.tokens) return;     // whole waves; no barrier when WPR == 1
   const int d = a.d;
+  const bool out = a.h || a.out.codes;
   const T *r = static_cast<const T *>(a.r) + t * a.ld_r;
+  Pack8<T> kr[NCH];
+  NormWeights<E, WB, WPR, NCH> pre;
   float v[NCH][8];               // r, then r', then h
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int e0 = 8 * (c * 64 * WPR + lane);
-    load8(r + min(e0, d - 1), d - e0, v[c]);
-  }
   if (a.b) {
     const T *b = static_cast<const T *>(a.b) + t * a.ld_b;
+    const T *g = static_cast<const T *>(a.gate) +
+                 (a.gate ? int64_t(uint32_t(t) / uint32_t(a.gate_tokens)) * a.ld_gate : 0);
+    Pack8<T> kb[NCH], kg[NCH];
+    NormWeights<E, WB, WPR, NCH> post;
     float p[NCH][8];
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int e0 = 8 * (c * 64 * WPR + lane);
-      load8(b + min(e0, d - 1), d - e0, p[c]);
-    }
-    normalize<WPR, NCH>(p, a.post, a.post_w, a.post_b, a.w_type, a.offset, a.eps, d, lane,
-                        slots[0], slots[1]);
+    for (int c = 0; c < NCH; ++c) kb[c] = fetch8<E>(b, 8 * (c * 64 * WPR + lane), d);
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) kr[c] = fetch8<E>(r, 8 * (c * 64 * WPR + lane), d);
+    post.fetch(a.post_w, a.post_b, d, lane);
+    if (NCH == 1 && a.gate) kg[0] = fetch8<E>(g, 8 * lane, d);
+    if (NCH == 1 && out) pre.fetch(a.pre_w, a.pre_b, d, lane);
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) widen8<E>(kb[c], 8 * (c * 64 * WPR + lane), d, 0.f, p[c]);
+    normalize<E, WB, WPR, NCH>(p, a.post, post, a.post_w, a.post_b, a.w_type, a.offset, a.eps, d,
+                            lane, slots[0], slots[1]);
     if (a.gate) {
-      const T *g = static_cast<const T *>(a.gate) + (t / a.gate_tokens) * a.ld_gate;
+      if (NCH > 1)
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) kg[c] = fetch8<E>(g, 8 * (c * 64 * WPR + lane), d);
 #pragma unroll
       for (int c = 0; c < NCH; ++c) {
-        const int e0 = 8 * (c * 64 * WPR + lane);
         float f[8];
-        load8(g + min(e0, d - 1), d - e0, f);
+        widen8<E>(kg[c], 8 * (c * 64 * WPR + lane), d, 0.f, f);
 #pragma unroll
         for (int j = 0; j < 8; ++j) p[c][j] *= f[j];
       }
     }
 #pragma unroll
-    for (int c = 0; c < NCH; ++c)
+    for (int c = 0; c < NCH; ++c) {
+      widen8<E>(kr[c], 8 * (c * 64 * WPR + lane), d, 0.f, v[c]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[c][j] = a.alpha * v[c][j] + a.beta * p[c][j];
+    }
+    if (NCH > 1 && out) pre.fetch(a.pre_w, a.pre_b, d, lane);
   } else {
 #pragma unroll
-    for (int c = 0; c < NCH; ++c)
+    for (int c = 0; c < NCH; ++c) kr[c] = fetch8<E>(r, 8 * (c * 64 * WPR + lane), d);
+    if (out) pre.fetch(a.pre_w, a.pre_b, d, lane);
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      widen8<E>(kr[c], 8 * (c * 64 * WPR + lane), d, 0.f, v[c]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[c][j] *= a.alpha;
+    }
   }
   if (a.r_out) {
     T *o = static_cast<T *>(a.r_out) + t * a.ld_r_out;
@@ -248,9 +301,9 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) norm_block_kernel(N
       if (e0 < d) store8(o + e0, d - e0, v[c]);
     }
   }
-  if (!a.h && !a.out.codes) return;
-  normalize<WPR, NCH>(v, a.pre, a.pre_w, a.pre_b, a.w_type, a.offset, a.eps, d, lane, slots[2],
-                      slots[3]);
+  if (!out) return;
+  normalize<E, WB, WPR, NCH>(v, a.pre, pre, a.pre_w, a.pre_b, a.w_type, a.offset, a.eps, d, lane,
+                          slots[2], slots[3]);
   if (a.h) {
     T *o = static_cast<T *>(a.h) + t * a.ld_h;
 #pragma unroll
@@ -266,33 +319,42 @@ __global__ void __launch_bounds__(WPR == 1 ? 256 : 64 * WPR) norm_block_kernel(N
 
 // ------------------------------------------------------------- launch rules
 // Waves per row and 8-element chunks per lane for rows of `n` elements.  Few
-// rows: as many waves as the row can use, one chunk per lane, so a row's
-// loads are in flight at once.  Many rows: four chunks per lane and fewer
-// waves (a narrow row on a single wave, without barriers).
+// rows take more waves and fewer chunks, which shortens the chain of loads and
+// reductions; many rows two chunks and fewer waves (a narrow row a single
+// wave, without barriers).
 struct RowShape {
   int wpr, nch;
 };
 RowShape row_shape(int64_t n, int64_t rows, int cus) {
   const int64_t lanes = cdiv(n, 8);
-  if (rows >= 4 * cus) {
-    if (lanes <= 64 * 4) return {1, lanes <= 64 ? 1 : 4};
-    if (lanes <= 256 * 4) return {4, 4};
-    if (lanes <= 512 * 4) return {8, 4};
-    return {16, 4};
-  }
+  const bool many = rows >= 4 * cus;
   if (lanes <= 64) return {1, 1};
+  if (many && lanes <= 128) return {1, 2};
   if (lanes <= 256) return {4, 1};
-  if (lanes <= 512) return {8, 1};
-  if (lanes <= 1024) return {16, 1};
-  return {16, 4};
+  if (lanes <= 512) return many ? RowShape{4, 2} : RowShape{8, 1};
+  if (lanes <= 1024) return {8, 2};
+  return {16, lanes <= 2048 ? 2 : 4};
 }
 
-template <typename F>
+template <Ends E, typename F>
 gptq_status with_shape(RowShape s, F &&f) {
-  if (s.wpr == 1) return s.nch == 1 ? f.template operator()<1, 1>() : f.template operator()<1, 4>();
-  if (s.wpr == 4) return s.nch == 1 ? f.template operator()<4, 1>() : f.template operator()<4, 4>();
-  if (s.wpr == 8) return s.nch == 1 ? f.template operator()<8, 1>() : f.template operator()<8, 4>();
-  return s.nch == 1 ? f.template operator()<16, 1>() : f.template operator()<16, 4>();
+  switch (s.wpr * 8 + s.nch) {
+    case 1 * 8 + 1: return f.template operator()<E, 1, 1>();
+    case 1 * 8 + 2: return f.template operator()<E, 1, 2>();
+    case 4 * 8 + 1: return f.template operator()<E, 4, 1>();
+    case 4 * 8 + 2: return f.template operator()<E, 4, 2>();
+    case 8 * 8 + 1: return f.template operator()<E, 8, 1>();
+    case 8 * 8 + 2: return f.template operator()<E, 8, 2>();
+    case 16 * 8 + 2: return f.template operator()<E, 16, 2>();
+    default: return f.template operator()<E, 16, 4>();
+  }
+}
+// `d`: the row's width; `n`: the elements its lanes have to cover.
+template <typename F>
+gptq_status with_row(int64_t d, int64_t n, int64_t rows, F &&f) {
+  const RowShape s = row_shape(n, rows, device_cu_count());
+  if (ends_of(d) == kShort) return f.template operator()<kShort, 1, 1>();
+  return ends_of(d) == kRagged ? with_shape<kRagged>(s, f) : with_shape<kWhole>(s, f);
 }
 
 template <typename T>
@@ -302,13 +364,21 @@ struct LaunchQuantize {
   CodesOut out;
   hipStream_t s;
   const char *name;
-  template <int WPR, int NCH>
+  template <Ends E, int WPR, int NCH>
   gptq_status operator()() {
     const dim3 grid(uint32_t(cdiv(tokens, WPR == 1 ? 4 : 1))), block(WPR == 1 ? 256 : 64 * WPR);
-    return u ? launch(name, quantize_kernel<T, WPR, NCH, true>, grid, block, 0, s, x, u, tokens,
+    return u ? launch(name, quantize_kernel<T, E, WPR, NCH, true>, grid, block, 0, s, x, u, tokens,
                       int(cols), ld, out)
-             : launch(name, quantize_kernel<T, WPR, NCH, false>, grid, block, 0, s, x, u, tokens,
-                      int(cols), ld, out);
+             : launch(name, quantize_kernel<T, E, WPR, NCH, false>, grid, block, 0, s, x, u,
+                      tokens, int(cols), ld, out);
+  }
+  template <Ends E>
+  gptq_status wide() {
+    const dim3 grid{uint32_t(tokens)};
+    return u ? launch(name, quantize_wide_kernel<T, E, true>, grid, dim3(1024), 0, s, x, u, tokens,
+                      int(cols), ld, out)
+             : launch(name, quantize_wide_kernel<T, E, false>, grid, dim3(1024), 0, s, x, u,
+                      tokens, int(cols), ld, out);
   }
 };
 
@@ -317,29 +387,27 @@ gptq_status quantize_typed(const void *x, const void *u, int64_t tokens, int64_t
                            const CodesOut &out, hipStream_t s, const char *name) {
   LaunchQuantize<T> l{static_cast<const T *>(x), static_cast<const T *>(u), tokens, cols, ld, out,
                       s, name};
-  if (out.pad <= 32768) return with_shape(row_shape(out.pad, tokens, device_cu_count()), l);
-  return u ? launch(name, quantize_wide_kernel<T, true>, dim3(uint32_t(tokens)), dim3(1024), 0, s,
-                    l.x, l.u, tokens, int(cols), ld, out)
-           : launch(name, quantize_wide_kernel<T, false>, dim3(uint32_t(tokens)), dim3(1024), 0,
-                    s, l.x, l.u, tokens, int(cols), ld, out);
+  if (out.pad <= 32768) return with_row(cols, out.pad, tokens, l);
+  return ends_of(cols) == kRagged ? l.template wide<kRagged>() : l.template wide<kWhole>();
 }
 
 template <typename T>
 struct LaunchNorm {
   const NormArgs &a;
   hipStream_t s;
-  template <int WPR, int NCH>
+  template <Ends E, int WPR, int NCH>
   gptq_status operator()() {
-    return launch("norm_block", norm_block_kernel<T, WPR, NCH>,
-                  dim3(uint32_t(cdiv(a.tokens, WPR == 1 ? 4 : 1))),
-                  dim3(WPR == 1 ? 256 : 64 * WPR), 0, s, a);
+    const dim3 grid(uint32_t(cdiv(a.tokens, WPR == 1 ? 4 : 1))), block(WPR == 1 ? 256 : 64 * WPR);
+    return a.w_type == GPTQ_DT_F32
+               ? launch("norm_block", norm_block_kernel<T, E, 4, WPR, NCH>, grid, block, 0, s, a)
+               : launch("norm_block", norm_block_kernel<T, E, 2, WPR, NCH>, grid, block, 0, s, a);
   }
 };
 
 template <typename T>
 gptq_status norm_typed(const NormArgs &a, hipStream_t s) {
   const int64_t n = a.out.codes ? std::max<int64_t>(a.d, a.out.pad) : a.d;
-  return with_shape(row_shape(n, a.tokens, device_cu_count()), LaunchNorm<T>{a, s});
+  return with_row(a.d, n, a.tokens, LaunchNorm<T>{a, s});
 }
 
 gptq_status check_codes(const int8_t *codes, int64_t ld_codes, int64_t cols, const float *scale,
@@ -466,7 +534,7 @@ gptq_status gptq_norm_block(const gptq_norm_params *p, int32_t dtype, int64_t to
     a.ld_gate = ld_gate;
     a.ld_r_out = ld_r_out;
     a.ld_h = ld_h;
-    a.gate_tokens = gate_tokens;
+    a.gate_tokens = std::min<int64_t>(std::max<int64_t>(gate_tokens, 1), tokens);   // 32 bits
     a.tokens = tokens;
     a.post_w = p->post_weight;
     a.post_b = p->post_bias;

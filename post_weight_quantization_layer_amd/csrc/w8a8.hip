@@ -198,9 +198,10 @@ __device__ __forceinline__ void lds_barrier() {
 // Iteration u: step 0 multiplies the first 64 k of stage u (set X) while the
 // second 64 k (set Y) are read; a barrier makes stage u + 1 visible; step 1
 // multiplies set Y while set X is read from stage u + 1.  Each of a stage's
-// copies waits in a register from its load to its store one to two steps
-// later, into the ring slot whose last reads came before the previous
-// barrier.
+// copies waits in registers from its load to its store DEPTH stages later,
+// into the ring slot whose last reads came before the previous barrier.
+// Small tiles, whose stages are shorter than a memory access, take DEPTH 2
+// or 3; 256 x 256 tiles have registers for 1.
 __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
 
 // Tiles in bands of kBand token tiles, tokens fastest: workgroups are dealt
@@ -240,7 +241,7 @@ __device__ __forceinline__ void settle(i32x4_t (&acc)[FA][FB]) {
     for (int j = 0; j < FB; ++j) asm volatile("" : "+a"(acc[i][j]));
 }
 
-template <int FA, int FB, bool SPLIT>
+template <int FA, int FB, int DEPTH, bool SPLIT>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FA * FB > 16 ? 1 : 2)))
     w8a8_tile_kernel(GemmArgs a, int token_tiles, int row_tiles, int splits) {
   constexpr int kWBytes = 32 * FA * kStep, kXBytes = 32 * FB * kStep;
@@ -278,19 +279,19 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FA 
   }
   const int xrow = tid >> 3;
   const int lds_x = kWBytes + xrow * kStep + (((tid & 7) ^ swz(xrow)) << 4);
-  u32x4r_t stg[kLoads];
-  auto load_one = [&](int q, int t) {
+  u32x4r_t stg[DEPTH][kLoads];   // copies of stage t wait in set t % DEPTH
+  auto load_one = [&](int q, int t, int set) {
     t = min(t, U - 1);
     auto base = (const __attribute__((address_space(1))) int8_t *)(
         q < kWLoads ? wbase + int64_t(t) * 2048 : xbase + int64_t(t) * kStep);
     uint32_t off = voff[q];
     asm("" : "+s"(base), "+v"(off));   // scalar base, the lane's fixed 32-bit offset
-    stg[q] = *(const __attribute__((address_space(1))) u32x4r_t *)(base + off);
+    stg[set][q] = *(const __attribute__((address_space(1))) u32x4r_t *)(base + off);
   };
-  auto store_one = [&](int q, int t) {
+  auto store_one = [&](int q, int t, int set) {
     uint8_t *p = smem + (t & 1) * kStageBytes +
                  (q < kWLoads ? q * 4096 + tid * 16 : lds_x + (q - kWLoads) * 32 * kStep);
-    *reinterpret_cast<u32x4r_t *>(p) = stg[q];
+    *reinterpret_cast<u32x4r_t *>(p) = stg[set][q];
   };
   auto frag_a = [&](int u, int h, int i) {
     return *reinterpret_cast<const i32x4_t *>(smem + (u & 1) * kStageBytes +
@@ -308,17 +309,22 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FA 
 #pragma unroll
     for (int j = 0; j < FB; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
   i32x4_t xa[4], xb[FB], ya[FA], yb[FB];   // xa: block row i in slot i % 4
+  // Copies below kHalf run one stage ahead of the others: stages 0 and 1 of
+  // them are stored here, stage 0 of the others; then each has DEPTH stages
+  // in flight.
 #pragma unroll
-  for (int q = 0; q < kLoads; ++q) load_one(q, 0);
+  for (int t = 0; t < DEPTH; ++t)
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) load_one(q, t, t);
 #pragma unroll
   for (int q = 0; q < kLoads; ++q) {
-    store_one(q, 0);
-    load_one(q, 1);
+    store_one(q, 0, 0);
+    load_one(q, DEPTH, 0);
   }
 #pragma unroll
   for (int q = 0; q < kHalf; ++q) {
-    store_one(q, 1);
-    load_one(q, 2);
+    store_one(q, 1, 1 % DEPTH);
+    load_one(q, 1 + DEPTH, 1 % DEPTH);
   }
   lds_barrier();
 #pragma unroll
@@ -331,7 +337,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FA 
   constexpr int kY = FA + FB, kYEvery = kSlots / kY;       // reads of set Y in step 0
   constexpr int kX = FB + 3, kXEvery = kSlots / kX;        // reads of set X in step 1
   constexpr int kCEvery = kSlots / kHalf;                  // copies in either step
-  for (int u = 0; u < U; ++u) {
+  auto stage = [&](int u, int ph) {    // ph = u % DEPTH
 #pragma unroll
     for (int i = 0; i < FA; ++i)
 #pragma unroll
@@ -346,8 +352,8 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FA 
           else ya[f - FB] = frag_a(u, 1, f - FB);
         }
         if (q % kCEvery == kCEvery - 1 && q / kCEvery < kHalf) {
-          store_one(kHalf + q / kCEvery, u + 1);
-          load_one(kHalf + q / kCEvery, u + 2);
+          store_one(kHalf + q / kCEvery, u + 1, (ph + 1) % DEPTH);
+          load_one(kHalf + q / kCEvery, u + 1 + DEPTH, (ph + 1) % DEPTH);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -365,12 +371,20 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, FA 
           else xa[f - FB] = frag_a(u + 1, 0, f - FB);
         }
         if (q % kCEvery == kCEvery - 1 && q / kCEvery < kHalf) {
-          store_one(q / kCEvery, u + 2);
-          load_one(q / kCEvery, u + 3);
+          store_one(q / kCEvery, u + 2, (ph + 2) % DEPTH);
+          load_one(q / kCEvery, u + 2 + DEPTH, (ph + 2) % DEPTH);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+  };
+  int u = 0;
+  for (; u + DEPTH <= U; u += DEPTH) {
+#pragma unroll
+    for (int ph = 0; ph < DEPTH; ++ph) stage(u + ph, ph);
   }
+#pragma unroll
+  for (int ph = 0; ph < DEPTH - 1; ++ph)
+    if (u + ph < U) stage(u + ph, ph);
   settle<FA, FB>(acc);
   if (SPLIT) {
     // A wave's blocks as they lie in its registers: 1 KiB per store.
@@ -421,35 +435,21 @@ __global__ void __launch_bounds__(256)
 // once, so the product runs at the rate the weights arrive.  The waves'
 // sums meet in LDS.
 //
-// Tokens come as codes from memory (every workgroup reads them all, from its
-// XCD's L2), or, FUSED, as activations that each workgroup quantizes into LDS
-// itself while its first weights are on their way: that repeats a small
-// quantization per 16 rows but saves a launch.
-// Steps loaded at a time, two such sets in flight: what fits 128 registers a
-// lane with 16 waves (256 with fewer) beside the tokens' codes.
-constexpr int ahead(int waves, int nb, bool fused) {
-  return fused ? 4 : nb == 1 ? (waves == 16 ? 2 : 4) : (waves == 16 ? 1 : 2);
-}
-constexpr int kFusedChunks = 4;  // 8-element chunks of activations a lane may hold
+// (Quantizing the activations in each workgroup, to save a launch, was slower:
+// 1 x 28672 x 8192 took 54 us against 47 with the separate launch, 1 x 14336 x
+// 4096 21.8 against 15.2.)
+// Four waves: with 8 or 16 fewer workgroups fit a compute unit, and the tail
+// of one is not covered by others (16 x 14336 x 4096: 12, 22 and 22 us).
+constexpr int kRowsWaves = 4;
 
-struct RowsFused {
-  const void *x;
-  int64_t ld;
-  int cols;
-};
-
-template <typename T, int WAVES, int NB, bool FUSED>
-__global__ void __launch_bounds__(64 * WAVES) w8a8_rows_kernel(GemmArgs a, RowsFused f) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kThreads = 64 * WAVES, kAhead = ahead(WAVES, NB, FUSED);
+template <int NB>
+__global__ void __launch_bounds__(64 * kRowsWaves) w8a8_rows_kernel(GemmArgs a) {
+  constexpr int WAVES = kRowsWaves, kThreads = 64 * WAVES;
+  __shared__ i32x4_t sums[WAVES * NB * 64];
+  constexpr int kAhead = NB == 1 ? 4 : 2;   // steps loaded at a time, two such sets in flight
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rt = blockIdx.x;
-  const int k_pad = a.steps * kStep, ld_lds = k_pad + 16;
-  i32x4_t *sums = reinterpret_cast<i32x4_t *>(smem);                    // WAVES x NB KiB
-  int8_t *codes = reinterpret_cast<int8_t *>(smem + WAVES * NB * 1024);  // FUSED: tokens rows
-  __shared__ uint32_t slot_max[16][WAVES];
-  __shared__ int slot_sum[16][WAVES];
 
   // This wave's steps: wave, wave + WAVES, ...  Loads past the last repeat it.
   const int n = (a.steps - wave + WAVES - 1) / WAVES;
@@ -458,11 +458,10 @@ __global__ void __launch_bounds__(64 * WAVES) w8a8_rows_kernel(GemmArgs a, RowsF
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
     const int t = min(16 * j + (lane & 15), a.tokens - 1);
-    xrow[j] = FUSED ? codes + t * ld_lds + (lane >> 4) * 16
-                    : a.x + int64_t(t) * a.ld_x + (lane >> 4) * 16;
+    xrow[j] = a.x + int64_t(t) * a.ld_x + (lane >> 4) * 16;
   }
   struct Set {
-    i32x4_t w[kAhead][2], x[FUSED ? 1 : kAhead][2][NB];
+    i32x4_t w[kAhead][2], x[kAhead][2][NB];
   };
   auto load = [&](Set &b, int at) {
 #pragma unroll
@@ -471,11 +470,9 @@ __global__ void __launch_bounds__(64 * WAVES) w8a8_rows_kernel(GemmArgs a, RowsF
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         b.w[i][h] = *reinterpret_cast<const i32x4_t *>(w + s * 2048 + h * 1024);
-        if (!FUSED)
 #pragma unroll
-          for (int j = 0; j < NB; ++j)
-            b.x[FUSED ? 0 : i][h][j] =
-                *reinterpret_cast<const i32x4_t *>(xrow[j] + s * kStep + h * 64);
+        for (int j = 0; j < NB; ++j)
+          b.x[i][h][j] = *reinterpret_cast<const i32x4_t *>(xrow[j] + s * kStep + h * 64);
       }
     }
   };
@@ -486,61 +483,17 @@ __global__ void __launch_bounds__(64 * WAVES) w8a8_rows_kernel(GemmArgs a, RowsF
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (at + i >= n) break;
-      const int s = wave + (at + i) * WAVES;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const i32x4_t xf = FUSED ? *reinterpret_cast<const i32x4_t *>(xrow[j] + s * kStep + h * 64)
-                                   : b.x[FUSED ? 0 : i][h][j];
-          acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b.w[i][h], xf, acc[j], 0, 0, 0);
-        }
+        for (int j = 0; j < NB; ++j)
+          acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b.w[i][h], b.x[i][h][j], acc[j], 0, 0, 0);
     }
   };
   Set s0, s1;
   if (n > 0) {
     load(s0, 0);
     load(s1, kAhead);
-  }
-  if (FUSED) {
-    // Chunk c of a lane: token c / per, elements 8 (c % per * threads + tid).
-    const int per = (k_pad + 8 * kThreads - 1) / (8 * kThreads);
-    float v[kFusedChunks][8];
-#pragma unroll
-    for (int c = 0; c < kFusedChunks; ++c) {
-      const int t = c / per, e0 = 8 * (c % per * kThreads + tid);
-      if (t < a.tokens)
-        load8(static_cast<const T *>(f.x) + t * f.ld + min(e0, f.cols - 1), f.cols - e0, v[c]);
-    }
-#pragma unroll
-    for (int c = 0; c < kFusedChunks; ++c) {
-      const int t = c / per;
-      if (t >= a.tokens) break;
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = MaxU::op(m, __float_as_uint(v[c][j]) & 0x7fffffffu);
-      m = wave_all<MaxU>(m);
-      if (lane == 0) slot_max[c][wave] = m;
-    }
-    lds_barrier();
-#pragma unroll
-    for (int c = 0; c < kFusedChunks; ++c) {
-      const int t = c / per, e0 = 8 * (c % per * kThreads + tid);
-      if (t >= a.tokens) break;
-      uint32_t m = 0;
-      for (int p = 0; p < per; ++p)
-#pragma unroll
-        for (int i = 0; i < WAVES; ++i) m = MaxU::op(m, slot_max[t * per + p][i]);
-      const float s = row_scale(m);
-      int q[8] = {0, 0, 0, 0, 0, 0, 0, 0}, total = 0;
-      if (s > 0.f) codes8(v[c], s, 1.f / s, q);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) total += q[j];
-      if (e0 < k_pad) *reinterpret_cast<u32x2_t *>(codes + t * ld_lds + e0) = pack_codes8(q);
-      total = wave_all<SumI>(total);
-      if (lane == 0) slot_sum[c][wave] = total;
-    }
-    lds_barrier();
   }
   for (int at = 0; at < n; at += 2 * kAhead) {
     multiply(s0, at);
@@ -560,24 +513,9 @@ __global__ void __launch_bounds__(64 * WAVES) w8a8_rows_kernel(GemmArgs a, RowsF
     uint32_t total = 0;
 #pragma unroll
     for (int i = 0; i < WAVES; ++i) total += uint32_t(flat[i * NB * 256 + at]);
-    float st;
-    uint32_t sum = 0;
-    if (FUSED) {
-      const int per = (k_pad + 8 * kThreads - 1) / (8 * kThreads);
-      uint32_t m = 0;
-      for (int p = 0; p < per; ++p)
-#pragma unroll
-        for (int i = 0; i < WAVES; ++i) {
-          m = MaxU::op(m, slot_max[t * per + p][i]);
-          sum += uint32_t(slot_sum[t * per + p][i]);
-        }
-      st = row_scale(m);
-    } else {
-      st = a.x_scale[t];
-      sum = uint32_t(a.x_sum[t]);
-    }
     if (row >= a.rows) continue;
-    float y = float(int(total - uint32_t(a.w_shift[row]) * sum)) * (st * a.w_scale[row]);
+    float y = float(int(total - uint32_t(a.w_shift[row]) * uint32_t(a.x_sum[t]))) *
+              (a.x_scale[t] * a.w_scale[row]);
     asm("" : "+v"(y));    // rounded to float32 before it is narrowed
     const int64_t to = int64_t(t) * a.ld_y + row;
     if (a.y_type == GPTQ_DT_F32) static_cast<float *>(a.y)[to] = y;
@@ -623,44 +561,65 @@ gptq_status check_scratch(const void *ws, size_t ws_bytes, size_t need) {
 }
 
 // ------------------------------------------------------------- launch rules
-// How a product of `tokens` tokens runs: on the rows kernel (waves > 0), or
-// on tiles of 32 fa rows x 32 fb tokens, k in `splits` parts.
+// How a product of `tokens` tokens runs: on the rows kernel, or on tiles of
+// 32 fa rows x 32 fb tokens, k in `splits` parts.
 struct Plan {
-  int waves, fa, fb, splits;
+  bool rows;
+  int fa, fb, splits;
 };
 
 Plan plan_for(const Geometry &g, int64_t tokens, int cus) {
   const int steps = int(g.k_pad / kStep);
-  if (tokens <= 32) {
-    // Enough waves to hold a row tile's k in flight; fewer, smaller
-    // workgroups where there are many row tiles.
-    const int64_t rt = g.rows_pad / 16;
-    int waves = rt >= 4 * cus ? 4 : rt >= 2 * cus ? 8 : 16;
-    while (waves < 16 && steps > waves * 16) waves *= 2;
-    while (waves > 4 && steps <= waves * 2) waves /= 2;
-    return {waves, 0, 0, 1};
+  // The rows kernel reads every token once per 16 rows, the 128 x 64 tiles
+  // once per 128 but with idle compute units below a tile per unit.  Measured
+  // (us, rows kernel / tiles): 8 x 28672 x 8192 42 / 43, 16 tokens 50 / 43,
+  // 32 tokens 67 / 43; 14336 x 4096: 16 tokens 12 / 15, 32 tokens 19 / 15;
+  // 8192 x 8192: 24 tokens 17 / 18.5; 4096 x 11008: 32 tokens 14 / 15.
+  const int64_t wide = cdiv(g.rows, 128);
+  if (tokens <= 8 || (tokens <= 16 && 10 * wide < 7 * cus) || (tokens <= 32 && 10 * wide < 4 * cus))
+    return {true, 0, 0, 1};
+  // Tiles: the shape and the split of the least modelled time.  A compute
+  // unit runs n = ceil(tiles splits / CUs) workgroups of steps / splits
+  // stages; a stage of a shape costs it `stage` us and a workgroup `fixed` us
+  // (first loads, epilogue; shared by `fit` resident workgroups); a split adds
+  // the join.  Larger tiles read less per product, smaller ones leave fewer
+  // compute units idle.  The figures are fits to measured products (us):
+  // 2048 x 22016 x 4096 took 177 on 256 x 256 tiles, 209 on 128 x 256; 2048 x
+  // 4096 x 11008 119 against 85 (90 on 128 x 128); 1024 x 4096 x 4096 33 on
+  // 128 x 256, 23 on 128 x 128; 512 x 4096 x 4096 21 on 128 x 128, 16 on
+  // 128 x 64; 128 x 4096 x 11008 29 on 128 x 64, 17 with k in four.
+  struct Shape {
+    int fa, fb, fit, most;
+    double stage, fixed;
+  };
+  constexpr Shape kShapes[] = {
+      {8, 8, 1, 1, 1.47, 12.8}, {4, 8, 1, 1, 0.92, 6}, {4, 4, 2, 8, 0.53, 5}, {4, 2, 3, 8, 0.33, 5}};
+  Plan best{false, 4, 2, 1};
+  double least = 1e30;
+  for (const Shape &sh : kShapes) {
+    const int64_t tiles = cdiv(g.rows, 32 * sh.fa) * cdiv(tokens, 32 * sh.fb);
+    for (int splits = 1; splits <= sh.most && splits * 4 <= std::max(steps, 4); ++splits) {
+      const int64_t n = cdiv(tiles * splits, cus);
+      double us = double(n * cdiv(steps, splits)) * sh.stage + double(cdiv(n, sh.fit)) * sh.fixed;
+      if (splits > 1) us += 4.5 + double(tiles * splits) * (32 * sh.fa * 32 * sh.fb) * 8e-6 / 4;
+      if (us < least) {
+        least = us;
+        best = {false, sh.fa, sh.fb, splits};
+      }
+    }
   }
-  const int64_t big = cdiv(g.rows, 256) * cdiv(tokens, 256);
-  if (big >= cus) return {0, 8, 8, 1};
-  const int64_t mid = cdiv(g.rows, 128) * cdiv(tokens, 256);
-  if (mid >= cus && tokens >= 192) return {0, 4, 8, 1};
-  if (tokens <= 64) {
-    const int64_t tiles = cdiv(g.rows, 128);
-    return {0, 4, 2, int(std::max<int64_t>(1, std::min<int64_t>(2 * cus / tiles, steps / 4)))};
-  }
-  const int64_t tiles = cdiv(g.rows, 128) * cdiv(tokens, 128);
-  return {0, 4, 4, int(std::max<int64_t>(1, std::min<int64_t>(2 * cus / tiles, steps / 4)))};
+  return best;
 }
 
 size_t part_bytes(const Geometry &g, int64_t tokens, const Plan &p) {
-  if (p.waves || p.splits == 1) return 0;
+  if (p.rows || p.splits == 1) return 0;
   return align256(size_t(cdiv(g.rows, 32 * p.fa) * cdiv(tokens, 32 * p.fb)) * p.splits *
                   (32 * p.fa * 32 * p.fb * sizeof(int32_t)));
 }
 
-template <int FA, int FB, bool SPLIT>
+template <int FA, int FB, int DEPTH, bool SPLIT>
 gptq_status launch_tiles(const GemmArgs &a, int splits, hipStream_t s) {
-  auto kern = w8a8_tile_kernel<FA, FB, SPLIT>;
+  auto kern = w8a8_tile_kernel<FA, FB, DEPTH, SPLIT>;
   const size_t lds = size_t(2) * 32 * (FA + FB) * kStep;
   GPTQ_TRY(allow_dynamic_lds(reinterpret_cast<const void *>(kern), lds));
   const int rt = int(cdiv(a.rows, 32 * FA)), tt = int(cdiv(a.tokens, 32 * FB));
@@ -671,71 +630,38 @@ gptq_status launch_tiles(const GemmArgs &a, int splits, hipStream_t s) {
                 rt, splits);
 }
 
-template <typename T, int WAVES, int NB, bool FUSED>
-gptq_status launch_rows(const GemmArgs &a, const RowsFused &f, hipStream_t s) {
-  auto kern = w8a8_rows_kernel<T, WAVES, NB, FUSED>;
-  const size_t lds = size_t(WAVES) * NB * 1024 +
-                     (FUSED ? size_t(a.tokens) * (a.steps * kStep + 16) : 0);
-  GPTQ_TRY(allow_dynamic_lds(reinterpret_cast<const void *>(kern), 96 * 1024));
-  return launch("w8a8_rows", kern, dim3(uint32_t(a.row_tiles)), dim3(64 * WAVES), lds, s, a, f);
-}
-template <typename T, int NB, bool FUSED>
-gptq_status launch_rows_waves(const GemmArgs &a, const RowsFused &f, int waves, hipStream_t s) {
-  if (waves == 4) return launch_rows<T, 4, NB, FUSED>(a, f, s);
-  if (waves == 8) return launch_rows<T, 8, NB, FUSED>(a, f, s);
-  return launch_rows<T, 16, NB, FUSED>(a, f, s);
-}
-
-// Whether each workgroup quantizes the activations itself: all tokens' chunks
-// fit in a lane's registers (then their codes, at most 4 * 8 * threads bytes,
-// fit in LDS too).
-bool fused_fits(const Geometry &g, int64_t tokens, const Plan &p) {
-  return p.waves && tokens * cdiv(g.k_pad, 8 * 64 * p.waves) <= kFusedChunks;
-}
-
-GemmArgs layer_args(const gptq_w8a8_layer *l, const Geometry &g, int64_t tokens, void *y,
-                    int32_t y_dtype, int64_t ld_y) {
+gptq_status gemm_launch(const gptq_w8a8_layer *l, const int8_t *codes, int64_t ld_codes,
+                        const float *scale, const int32_t *sum, int64_t tokens, void *y,
+                        int32_t y_dtype, int64_t ld_y, void *ws, hipStream_t s) {
+  const Geometry g = geometry(l->rows, l->cols);
   const LayerMap m = layer_map(l->mem, g);
   GemmArgs a;
   a.w = m.w;
   a.w_scale = m.scale;
   a.w_shift = m.shift;
-  a.x = nullptr;
-  a.x_scale = nullptr;
-  a.x_sum = nullptr;
+  a.x = codes;
+  a.x_scale = scale;
+  a.x_sum = sum;
   a.y = y;
-  a.ld_x = 0;
+  a.ld_x = ld_codes;
   a.ld_y = ld_y;
   a.tokens = int(tokens);
   a.rows = int(g.rows);
   a.row_tiles = int(g.rows_pad / 16);
   a.steps = int(g.k_pad / kStep);
   a.y_type = y_dtype;
-  a.part = nullptr;
-  return a;
-}
-
-gptq_status gemm_launch(const gptq_w8a8_layer *l, const int8_t *codes, int64_t ld_codes,
-                        const float *scale, const int32_t *sum, int64_t tokens, void *y,
-                        int32_t y_dtype, int64_t ld_y, void *ws, hipStream_t s) {
-  const Geometry g = geometry(l->rows, l->cols);
-  GemmArgs a = layer_args(l, g, tokens, y, y_dtype, ld_y);
-  a.x = codes;
-  a.x_scale = scale;
-  a.x_sum = sum;
-  a.ld_x = ld_codes;
   a.part = static_cast<i32x4_t *>(ws);
   const Plan p = plan_for(g, tokens, device_cu_count());
-  if (p.waves)
-    return tokens <= 16 ? launch_rows_waves<f16_t, 1, false>(a, RowsFused{}, p.waves, s)
-                        : launch_rows_waves<f16_t, 2, false>(a, RowsFused{}, p.waves, s);
-  if (p.fa == 8) return launch_tiles<8, 8, false>(a, 1, s);
-  if (p.fb == 8) return launch_tiles<4, 8, false>(a, 1, s);
+  if (p.rows)
+    return launch("w8a8_rows", tokens <= 16 ? w8a8_rows_kernel<1> : w8a8_rows_kernel<2>,
+                  dim3(uint32_t(a.row_tiles)), dim3(64 * kRowsWaves), 0, s, a);
+  if (p.fa == 8) return launch_tiles<8, 8, 1, false>(a, 1, s);
+  if (p.fb == 8) return launch_tiles<4, 8, 1, false>(a, 1, s);
   if (p.fb == 2)
-    return p.splits > 1 ? launch_tiles<4, 2, true>(a, p.splits, s)
-                        : launch_tiles<4, 2, false>(a, 1, s);
-  return p.splits > 1 ? launch_tiles<4, 4, true>(a, p.splits, s)
-                      : launch_tiles<4, 4, false>(a, 1, s);
+    return p.splits > 1 ? launch_tiles<4, 2, 3, true>(a, p.splits, s)
+                        : launch_tiles<4, 2, 3, false>(a, 1, s);
+  return p.splits > 1 ? launch_tiles<4, 4, 2, true>(a, p.splits, s)
+                      : launch_tiles<4, 4, 2, false>(a, 1, s);
 }
 
 }  // namespace
@@ -788,8 +714,6 @@ size_t gptq_w8a8_gemm_ws_bytes(const gptq_w8a8_layer *layer, int64_t tokens) {
 // scratch.
 size_t gptq_w8a8_linear_ws_bytes(const gptq_w8a8_layer *layer, int64_t tokens) {
   if (!layer || tokens < 1 || tokens > kMaxTokens) return 0;
-  const Geometry g = geometry(layer->rows, layer->cols);
-  if (fused_fits(g, tokens, plan_for(g, tokens, device_cu_count()))) return 0;
   return codes_bytes(layer, tokens) + 2 * align256(size_t(tokens) * 4) +
          gptq_w8a8_gemm_ws_bytes(layer, tokens);
 }
@@ -829,15 +753,6 @@ gptq_status gptq_w8a8_linear(const gptq_w8a8_layer *layer, const void *x, int32_
     GPTQ_TRY(check_output(layer, y, y_dtype, ld_y));
     GPTQ_TRY(check_scratch(ws, ws_bytes, gptq_w8a8_linear_ws_bytes(layer, tokens)));
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    const Geometry g = geometry(layer->rows, layer->cols);
-    const Plan plan = plan_for(g, tokens, device_cu_count());
-    if (fused_fits(g, tokens, plan)) {
-      const GemmArgs a = layer_args(layer, g, tokens, y, y_dtype, ld_y);
-      const RowsFused f{x, ld_x, int(layer->cols)};
-      if (x_dtype == GPTQ_DT_F32) return launch_rows_waves<float, 1, true>(a, f, plan.waves, s);
-      if (x_dtype == GPTQ_DT_BF16) return launch_rows_waves<bf16_t, 1, true>(a, f, plan.waves, s);
-      return launch_rows_waves<f16_t, 1, true>(a, f, plan.waves, s);
-    }
     char *p = static_cast<char *>(ws);
     int8_t *codes = reinterpret_cast<int8_t *>(p);
     float *scale = reinterpret_cast<float *>(p + codes_bytes(layer, tokens));
