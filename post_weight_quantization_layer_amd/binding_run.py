@@ -87,22 +87,30 @@ def _dtype(t: torch.Tensor, what: str) -> int:
         raise TypeError(f"{what} must be float32, bfloat16 or float16, not {t.dtype}") from None
 
 
-def stream_ptr(stream=None) -> int:
-    return torch.cuda.current_stream().cuda_stream if stream is None else \
-        getattr(stream, "cuda_stream", stream)
+def stream_ptr(t: torch.Tensor, stream=None) -> int:
+    """hipStream_t of ``stream``, or of the current stream of t's device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return getattr(stream, "cuda_stream", stream)
 
 
-def matrix(t: torch.Tensor, what: str, rows: int | None = None, cols: int | None = None):
-    """A device matrix whose rows are contiguous, of the given size where one is given."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+def matrix(t: torch.Tensor, what: str, rows: int | None = None, cols: int | None = None,
+           dtype: torch.dtype | None = None) -> tuple[int, int]:
+    """(address, row stride) of a device matrix whose rows are contiguous, of the
+    given size and type where one is given."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
         raise ValueError(f"{what} must be a matrix with contiguous rows, got shape "
-                         f"{tuple(t.shape)} and strides {t.stride()}")
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+                         f"{tuple(shape)} and strides {stride}")
+    r, c = shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{what} must be {'*' if rows is None else rows} x "
-                         f"{'*' if cols is None else cols}, got {tuple(t.shape)}")
+                         f"{'*' if cols is None else cols}, got {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{what} must be on the GPU")
-    return t
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    return t.data_ptr(), stride[0] if r > 1 else c    # torch may report any for one row
 
 
 def ld(t: torch.Tensor) -> int:
@@ -137,10 +145,12 @@ class Scratch:
         self.device = device
         self._by_stream: dict[int, torch.Tensor] = {}
 
-    def __call__(self, nbytes: int, ptr: int, stream=None) -> int | None:
-        """Address of at least ``nbytes`` bytes for use on the stream at ``ptr``."""
+    def __call__(self, nbytes: int, like: torch.Tensor, stream=None) -> int | None:
+        """Address of at least ``nbytes`` bytes for use on ``stream`` (None: the
+        current stream of ``like``'s device)."""
         if nbytes == 0:
             return None
+        ptr = stream_ptr(like, stream)
         t = self._by_stream.get(ptr)
         if t is None or t.numel() < nbytes:
             with on(stream):
@@ -158,20 +168,21 @@ def gptq_tokens_ld(cols: int) -> int:
 
 def gptq_quantize_tokens(x, codes, scale, sum, stream=None):
     """x tokens x cols float; codes tokens x ld int8; scale, sum: tokens float32 / int32."""
-    t, c = x.shape
-    _check(lib().gptq_quantize_tokens(x.data_ptr(), _dtype(x, "x"), t, c, ld(x), codes.data_ptr(),
+    ptr, stride = matrix(x, "x")
+    _check(lib().gptq_quantize_tokens(ptr, _dtype(x, "x"), *x.shape, stride, codes.data_ptr(),
                                       ld(codes), scale.data_ptr(), sum.data_ptr(),
-                                      stream_ptr(stream)))
+                                      stream_ptr(x, stream)))
 
 
 def gptq_silu_mul_quantize(g, u, codes, scale, sum, stream=None):
     """g, u tokens x cols of one type and row stride."""
-    t, c = g.shape
-    if u.dtype != g.dtype or u.shape != g.shape or ld(u) != ld(g):
-        raise ValueError("g and u must have one shape, type and row stride")
-    _check(lib().gptq_silu_mul_quantize(g.data_ptr(), u.data_ptr(), _dtype(g, "g"), t, c, ld(g),
+    ptr, stride = matrix(g, "g")
+    uptr, ustride = matrix(u, "u", *g.shape, g.dtype)
+    if ustride != stride:
+        raise ValueError("g and u must have one row stride")
+    _check(lib().gptq_silu_mul_quantize(ptr, uptr, _dtype(g, "g"), *g.shape, stride,
                                         codes.data_ptr(), ld(codes), scale.data_ptr(),
-                                        sum.data_ptr(), stream_ptr(stream)))
+                                        sum.data_ptr(), stream_ptr(g, stream)))
 
 
 def gptq_w8a8_layer_bytes(rows: int, cols: int) -> int:
@@ -188,7 +199,7 @@ def gptq_w8a8_prepare(q, scale, zero, mem, stream=None) -> gptq_w8a8_layer:
     layer = gptq_w8a8_layer()
     _check(lib().gptq_w8a8_prepare(q.data_ptr(), scale.data_ptr(), zero.data_ptr(), rows, cols,
                                    mem.data_ptr(), mem.numel() * mem.element_size(),
-                                   ctypes.byref(layer), stream_ptr(stream)))
+                                   ctypes.byref(layer), stream_ptr(q, stream)))
     return layer
 
 
@@ -200,32 +211,40 @@ def gptq_w8a8_linear_ws_bytes(layer: gptq_w8a8_layer, tokens: int) -> int:
     return lib().gptq_w8a8_linear_ws_bytes(layer, tokens)
 
 
-def gptq_w8a8_gemm(layer: gptq_w8a8_layer, codes, scale, sum, y, ws=None, tokens=None,
-                   stream=None):
-    n = 0 if ws is None else ws.numel() * ws.element_size()
+def gptq_w8a8_gemm(layer: gptq_w8a8_layer, codes, scale, sum, y, ws: int | None = None,
+                   ws_bytes: int = 0, stream=None):
+    """codes, scale, sum of y's tokens; y tokens x rows.  ``ws``: address."""
+    ptr, stride = matrix(y, "y", None, layer.rows)
     _check(lib().gptq_w8a8_gemm(layer, codes.data_ptr(), ld(codes), scale.data_ptr(),
-                                sum.data_ptr(), y.shape[0] if tokens is None else tokens,
-                                y.data_ptr(), _dtype(y, "y"), ld(y),
-                                None if ws is None else ws.data_ptr(), n, stream_ptr(stream)))
+                                sum.data_ptr(), y.shape[0], ptr, _dtype(y, "y"), stride, ws,
+                                ws_bytes, stream_ptr(y, stream)))
 
 
-def gptq_w8a8_linear(layer: gptq_w8a8_layer, x, y, ws=None, stream=None):
-    n = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(lib().gptq_w8a8_linear(layer, x.data_ptr(), _dtype(x, "x"), ld(x), x.shape[0],
-                                  y.data_ptr(), _dtype(y, "y"), ld(y),
-                                  None if ws is None else ws.data_ptr(), n, stream_ptr(stream)))
+def gptq_w8a8_linear(layer: gptq_w8a8_layer, x, y, ws: int | None = None, ws_bytes: int = 0,
+                     stream=None):
+    """x tokens x cols, y tokens x rows.  ``ws``: address."""
+    ptr, stride = matrix(x, "x", None, layer.cols)
+    tokens = x.shape[0]
+    yptr, ystride = matrix(y, "y", tokens, layer.rows)
+    _check(lib().gptq_w8a8_linear(layer, ptr, _dtype(x, "x"), stride, tokens, yptr,
+                                  _dtype(y, "y"), ystride, ws, ws_bytes, stream_ptr(x, stream)))
+
+
+_NONE = (None, 0)
 
 
 def gptq_norm_block(params: gptq_norm_params, r, b=None, gate=None, gate_tokens: int = 1,
                     r_out=None, h=None, codes=None, scale=None, sum=None, stream=None):
     t, d = r.shape
-
-    def at(x):
-        return (None, 0) if x is None else (x.data_ptr(), ld(x))
-
-    _check(lib().gptq_norm_block(params, _dtype(r, "r"), t, d, *at(r), *at(b), *at(gate),
-                                 gate_tokens, *at(r_out), *at(h), *at(codes),
-                                 B._ptr(scale), B._ptr(sum), stream_ptr(stream)))
+    kind = r.dtype
+    _check(lib().gptq_norm_block(
+        params, _dtype(r, "r"), t, d, *matrix(r, "r"),
+        *(_NONE if b is None else matrix(b, "b", t, d, kind)),
+        *(_NONE if gate is None else matrix(gate, "gate", None, d, kind)), gate_tokens,
+        *(_NONE if r_out is None else matrix(r_out, "r_out", t, d, kind)),
+        *(_NONE if h is None else matrix(h, "h", t, d, kind)),
+        *(_NONE if codes is None else (codes.data_ptr(), ld(codes))),
+        B._ptr(scale), B._ptr(sum), stream_ptr(r, stream)))
 
 
 def gptq_token_logprobs_ws_bytes(rows: int, vocab: int, top_k: int) -> int:
@@ -233,10 +252,10 @@ def gptq_token_logprobs_ws_bytes(rows: int, vocab: int, top_k: int) -> int:
 
 
 def gptq_token_logprobs(logits, ids, scale, top_k, logprob, rank, entropy, top_ids=None,
-                        top_logprobs=None, ws=None, stream=None):
-    rows, vocab = logits.shape
-    n = 0 if ws is None else ws.numel() * ws.element_size()
+                        top_logprobs=None, ws: int | None = None, ws_bytes: int = 0, stream=None):
+    """``ws``: address."""
+    ptr, stride = matrix(logits, "logits")
     _check(lib().gptq_token_logprobs(
-        logits.data_ptr(), _dtype(logits, "logits"), rows, vocab, ld(logits), B._ptr(ids), scale,
-        top_k, B._ptr(logprob), B._ptr(rank), B._ptr(entropy), B._ptr(top_ids),
-        B._ptr(top_logprobs), B._ptr(ws), n, stream_ptr(stream)))
+        ptr, _dtype(logits, "logits"), *logits.shape, stride, B._ptr(ids), scale, top_k,
+        B._ptr(logprob), B._ptr(rank), B._ptr(entropy), B._ptr(top_ids), B._ptr(top_logprobs),
+        ws, ws_bytes, stream_ptr(logits, stream)))

@@ -40,41 +40,30 @@ class NormBlock:
         None and b is given, not written if None and b is None).  h goes to
         ``h`` and / or, as codes, to ``codes``; the second result is ``codes``
         where only that is given, and a new tensor where neither is."""
-        R.matrix(r, "r", None, self.d)
+        if r.dim() != 2 or r.shape[1] != self.d:
+            raise ValueError(f"r must be tokens x {self.d}, got {tuple(r.shape)}")
         t = r.shape[0]
-        if b is not None:
-            R.matrix(b, "b", t, self.d)
-            if b.dtype != r.dtype:
-                raise TypeError("b must have the stream's type")
-        if gate is not None:
-            R.matrix(gate, "gate", None, self.d)
-            if gate.dtype != r.dtype:
-                raise TypeError("gate must have the stream's type")
+        if gate is None:
+            gate_tokens = 1
+        else:
             if gate_tokens is None:
                 gate_tokens = max(t, 1) if gate.shape[0] == 1 else 1
             if gate_tokens < 1 or gate.shape[0] * gate_tokens < t:
                 raise ValueError(f"{gate.shape[0]} gate rows of {gate_tokens} tokens do not "
                                  f"cover {t} tokens")
-        if r_out is None:
-            if b is not None:
-                with R.on(stream):
-                    r_out = torch.empty((t, self.d), dtype=r.dtype, device=r.device)
-        else:
-            R.matrix(r_out, "r_out", t, self.d)
-            if r_out.dtype != r.dtype:
-                raise TypeError("r_out must have the stream's type")
-        if h is None and codes is None:
+        if not r.is_cuda:
+            raise ValueError("r must be on the GPU")
+        if (r_out is None and b is not None) or (h is None and codes is None):
             with R.on(stream):
-                h = torch.empty((t, self.d), dtype=r.dtype, device=r.device)
-        elif h is not None:
-            R.matrix(h, "h", t, self.d)
-            if h.dtype != r.dtype:
-                raise TypeError("h must have the stream's type")
+                if r_out is None and b is not None:
+                    r_out = torch.empty((t, self.d), dtype=r.dtype, device=r.device)
+                if h is None and codes is None:
+                    h = torch.empty((t, self.d), dtype=r.dtype, device=r.device)
         c = s = n = None
         if codes is not None:
             if codes.cols != self.d:
                 raise ValueError(f"buffers for {codes.cols} features, got {self.d}")
             codes = codes.head(t)
             c, s, n = codes.codes, codes.scale, codes.sum
-        R.gptq_norm_block(self.params, r, b, gate, gate_tokens or 1, r_out, h, c, s, n, stream)
+        R.gptq_norm_block(self.params, r, b, gate, gate_tokens, r_out, h, c, s, n, stream)
         return r if r_out is None else r_out, codes if h is None else h

@@ -45,33 +45,31 @@ class TokenScorer:
         self.entropy = buffer(torch.float32, rows)
         self.top_ids = buffer(torch.int32, rows, top_k)
         self.top_logprobs = buffer(torch.float32, rows, top_k)
+        self._out = TokenLogprobs(self.logprob, self.rank, self.entropy, self.top_ids,
+                                  self.top_logprobs)
         self.scratch = R.Scratch(self.logprob.device)
+        self._last = (-1, 0)       # rows, scratch bytes
 
     def __call__(self, logits: torch.Tensor, ids: torch.Tensor | None = None, *,
                  scale: float = 1.0, stream=None) -> TokenLogprobs:
         """logits rows x vocab; ids rows int64 (negative: none given); ``scale``
         multiplies the logits (an inverse temperature)."""
-        R.matrix(logits, "logits", None, self.vocab)
+        if logits.dim() != 2 or logits.shape[1] != self.vocab:
+            raise ValueError(f"logits must be rows x {self.vocab}, got {tuple(logits.shape)}")
         n = logits.shape[0]
         if n > self.rows:
             raise ValueError(f"{n} rows asked of buffers for {self.rows}")
-        if ids is not None:
+        out = self._out if n == self.rows else TokenLogprobs(
+            *(None if t is None else t[:n] for t in (self.logprob, self.rank, self.entropy,
+                                                     self.top_ids, self.top_logprobs)))
+        if ids is None:
+            out = TokenLogprobs(None, None, out.entropy, out.top_ids, out.top_logprobs)
+        else:
             R.vector(ids, "ids", n, torch.int64)
-        whole = n == self.rows
-
-        def part(t):
-            return t if whole else t[:n]
-
-        out = TokenLogprobs(None if ids is None else part(self.logprob),
-                            None if ids is None else part(self.rank), part(self.entropy),
-                            part(self.top_ids), part(self.top_logprobs))
-        nbytes = R.lib().gptq_token_logprobs_ws_bytes(n, self.vocab, self.top_k)
-        ptr = R.stream_ptr(stream)
-        R._check(R.lib().gptq_token_logprobs(
-            logits.data_ptr(), R._dtype(logits, "logits"), n, self.vocab, R.ld(logits),
-            None if ids is None else ids.data_ptr(), scale, self.top_k,
-            None if ids is None else self.logprob.data_ptr(),
-            None if ids is None else self.rank.data_ptr(), self.entropy.data_ptr(),
-            self.top_ids.data_ptr(), self.top_logprobs.data_ptr(),
-            self.scratch(nbytes, ptr, stream), nbytes, ptr))
+        if self._last[0] != n:
+            self._last = (n, R.gptq_token_logprobs_ws_bytes(n, self.vocab, self.top_k))
+        nbytes = self._last[1]
+        R.gptq_token_logprobs(logits, ids, scale, self.top_k, out.logprob, out.rank, out.entropy,
+                              out.top_ids, out.top_logprobs,
+                              self.scratch(nbytes, logits, stream), nbytes, stream)
         return out

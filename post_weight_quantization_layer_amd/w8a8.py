@@ -41,16 +41,18 @@ class TokenCodes:
 
 
 def _for(x: torch.Tensor, out: TokenCodes | None, stream) -> TokenCodes:
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError("activations must be a tokens x features matrix on the GPU")
+    tokens, cols = x.shape
     if out is None:
-        return TokenCodes(x.shape[0], x.shape[1], x.device, stream)
-    if out.cols != x.shape[1]:
-        raise ValueError(f"buffers for {out.cols} features, got {x.shape[1]}")
-    return out.head(x.shape[0])
+        return TokenCodes(tokens, cols, x.device, stream)
+    if out.cols != cols:
+        raise ValueError(f"buffers for {out.cols} features, got {cols}")
+    return out.head(tokens)
 
 
 def quantize_tokens(x: torch.Tensor, out: TokenCodes | None = None, stream=None) -> TokenCodes:
     """x (tokens x features) as codes: scale max|x| / 127 per token."""
-    R.matrix(x, "x")
     out = _for(x, out, stream)
     R.gptq_quantize_tokens(x, out.codes, out.scale, out.sum, stream)
     return out
@@ -59,8 +61,6 @@ def quantize_tokens(x: torch.Tensor, out: TokenCodes | None = None, stream=None)
 def silu_mul_quantize(g: torch.Tensor, u: torch.Tensor, out: TokenCodes | None = None,
                       stream=None) -> TokenCodes:
     """silu(g) * u as codes; g and u may be the halves of one matrix."""
-    R.matrix(g, "g")
-    R.matrix(u, "u")
     out = _for(g, out, stream)
     R.gptq_silu_mul_quantize(g, u, out.codes, out.scale, out.sum, stream)
     return out
@@ -84,6 +84,7 @@ class W8A8Linear:
                                    dtype=torch.uint8, device=self.device)
         self.layer = R.gptq_w8a8_prepare(codes, scale, zero, self.mem, stream)
         self.scratch = R.Scratch(self.device)
+        self._last: dict = {}
 
     @classmethod
     def from_quantized(cls, *layers, stream=None) -> "W8A8Linear":
@@ -97,33 +98,38 @@ class W8A8Linear:
             return cls(torch.cat([q.q for q in layers]), torch.cat([q.scale for q in layers]),
                        torch.cat([q.zero for q in layers]), stream)
 
-    def _output(self, tokens: int, y, dtype, stream) -> torch.Tensor:
-        if y is None:
-            with R.on(stream):
-                return torch.empty((tokens, self.rows), dtype=dtype, device=self.device)
-        return R.matrix(y, "y", tokens, self.rows)
+    def _new(self, tokens: int, dtype, stream) -> torch.Tensor:
+        with R.on(stream):
+            return torch.empty((tokens, self.rows), dtype=dtype, device=self.device)
+
+    def _bytes(self, key: str, tokens: int) -> int:
+        """Scratch of a call, looked up once per token count in a row."""
+        last = self._last.get(key)
+        if last is None or last[0] != tokens:
+            last = (tokens, getattr(R, key)(self.layer, tokens))
+            self._last[key] = last
+        return last[1]
 
     def __call__(self, x: torch.Tensor, y: torch.Tensor | None = None, stream=None):
         """x tokens x cols -> y tokens x rows, of x's type unless ``y`` is given."""
-        R.matrix(x, "x", None, self.cols)
-        y = self._output(x.shape[0], y, x.dtype, stream)
-        n = R.lib().gptq_w8a8_linear_ws_bytes(self.layer, x.shape[0])
-        ptr = R.stream_ptr(stream)
-        R._check(R.lib().gptq_w8a8_linear(
-            self.layer, x.data_ptr(), R._dtype(x, "x"), R.ld(x), x.shape[0], y.data_ptr(),
-            R._dtype(y, "y"), R.ld(y), self.scratch(n, ptr, stream), n, ptr))
+        tokens = x.shape[0]
+        if y is None:
+            y = self._new(tokens, x.dtype, stream)
+        n = self._bytes("gptq_w8a8_linear_ws_bytes", tokens)
+        R.gptq_w8a8_linear(self.layer, x, y, self.scratch(n, self.mem, stream), n, stream)
         return y
 
     def product(self, tokens: TokenCodes, y: torch.Tensor | None = None,
                 dtype: torch.dtype = torch.float16, stream=None):
         """Token codes -> y tokens x rows (of ``dtype`` unless ``y`` is given)."""
+        t = tokens.tokens
         if tokens.cols != self.cols:
             raise ValueError(f"tokens of {tokens.cols} features, the layer takes {self.cols}")
-        y = self._output(tokens.tokens, y, dtype, stream)
-        n = R.lib().gptq_w8a8_gemm_ws_bytes(self.layer, tokens.tokens)
-        ptr = R.stream_ptr(stream)
-        R._check(R.lib().gptq_w8a8_gemm(
-            self.layer, tokens.codes.data_ptr(), R.ld(tokens.codes), tokens.scale.data_ptr(),
-            tokens.sum.data_ptr(), tokens.tokens, y.data_ptr(), R._dtype(y, "y"), R.ld(y),
-            self.scratch(n, ptr, stream), n, ptr))
+        if y is None:
+            y = self._new(t, dtype, stream)
+        elif y.shape[0] != t:
+            raise ValueError(f"y must have {t} rows, got {y.shape[0]}")
+        n = self._bytes("gptq_w8a8_gemm_ws_bytes", t)
+        R.gptq_w8a8_gemm(self.layer, tokens.codes, tokens.scale, tokens.sum, y,
+                         self.scratch(n, self.mem, stream), n, stream)
         return y
