@@ -196,17 +196,45 @@ __device__ __forceinline__ void widen_w(const RawW<WB> &r, int type, int e0, int
 struct SumF {
   __device__ static float op(float a, float b) { return a + b; }
 };
+struct MaxF {
+  __device__ static float op(float a, float b) { return fmaxf(a, b); }
+};
 struct SumI {
   __device__ static int op(int a, int b) { return a + b; }
 };
 struct MaxU {
   __device__ static uint32_t op(uint32_t a, uint32_t b) { return a > b ? a : b; }
 };
+struct MinU {
+  __device__ static uint32_t op(uint32_t a, uint32_t b) { return a < b ? a : b; }
+};
+struct OrU {
+  __device__ static uint32_t op(uint32_t a, uint32_t b) { return a | b; }
+};
+struct AndU {
+  __device__ static uint32_t op(uint32_t a, uint32_t b) { return a & b; }
+};
+template <int CTRL, typename V>
+__device__ __forceinline__ V dpp(V v) {
+  return __builtin_bit_cast(V, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf,
+                                                        true));
+}
+template <typename V>
+__device__ __forceinline__ V lane_value(V v, int lane) {
+  return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+// Over a wave, every lane active, in a fixed order; the result is uniform.
+// Within rows of 16 lanes by register moves between lanes (pairs, fours,
+// mirrored eights and sixteens), a few cycles each where an exchange through
+// LDS takes about a hundred; then the four rows' values as scalars.
 template <typename Op, typename V>
 __device__ __forceinline__ V wave_all(V v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v = Op::op(v, __shfl_xor(v, m));
-  return v;
+  v = Op::op(v, dpp<0xb1>(v));    // lanes 1 0 3 2
+  v = Op::op(v, dpp<0x4e>(v));    // lanes 2 3 0 1
+  v = Op::op(v, dpp<0x141>(v));   // mirrored in 8
+  v = Op::op(v, dpp<0x140>(v));   // mirrored in 16
+  return Op::op(Op::op(lane_value(v, 0), lane_value(v, 16)),
+                Op::op(lane_value(v, 32), lane_value(v, 48)));
 }
 // Over the row's WPR waves (the whole workgroup when WPR > 1): every thread
 // gets the value, combined in wave order.  `slot` is WPR words of LDS used

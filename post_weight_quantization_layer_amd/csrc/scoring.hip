@@ -26,6 +26,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kChunkElems = 8 * kThreads;   // elements a workgroup takes per chunk
 constexpr int kMaxTop = 64;
+constexpr int kUncut = 24;                  // shorter lists are not cut before the last step
 // A wave's list takes a whole chunk (512) on top of k cut entries.
 constexpr int kListCap = 512 + kMaxTop;
 
@@ -43,7 +44,7 @@ struct ScoreArgs {
   float *part;                  // splits > 1: per (row, split) kPartWords words
   uint64_t *part_keys;          //             and k keys
 };
-constexpr int kPartWords = 4;   // m, s, t, rank count
+constexpr int kPartWords = 8;   // m, s, t, rank count, the given token's logit
 
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -85,30 +86,29 @@ __device__ __forceinline__ float exponent(float l, float m, float c) {
 struct Stat {
   float m, s, t;
 };
-// Joins b into a.
-__device__ __forceinline__ void join(Stat &a, const Stat &b, float c) {
-  const float m = fmaxf(a.m, b.m), M = reference(m, c);
-  const bool plain = fabsf(M) < kLarge;
-  const float da = plain ? reference(a.m, c) - M : exponent(a.m, m, c);
-  const float db = plain ? reference(b.m, c) - M : exponent(b.m, m, c);
-  const float fa = exp2f(da), fb = exp2f(db);
-  // a part scaled to nothing adds nothing (its t would be 0 * infinity)
-  const float ta = fa > 0.f ? fa * (a.t + da * a.s) : 0.f;
-  const float tb = fb > 0.f ? fb * (b.t + db * b.s) : 0.f;
-  a = Stat{m, fa * a.s + fb * b.s, ta + tb};
+// The part at its own maximum, rescaled to the maximum m.
+__device__ __forceinline__ Stat rescaled(const Stat &a, float m, float c) {
+  const float M = reference(m, c);
+  const float d = fabsf(M) < kLarge ? reference(a.m, c) - M : exponent(a.m, m, c);
+  const float f = exp2f(d);
+  // a part scaled to nothing adds nothing (its t would be 0 * infinity); a NaN
+  // in s stays
+  return Stat{m, f * a.s, f > 0.f ? f * (a.t + d * a.s) : 0.f};
+}
+// Joins the lanes' statistics (uniform result).
+__device__ __forceinline__ Stat join_wave(const Stat &st, float c) {
+  const float m = wave_all<MaxF>(st.m);
+  const Stat r = rescaled(st, m, c);
+  return Stat{m, wave_all<SumF>(r.s), wave_all<SumF>(r.t)};
 }
 
-// Joins the lanes' statistics, in a fixed order.
-__device__ __forceinline__ void join_wave(Stat &st, float c) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const Stat o{__shfl_xor(st.m, m), __shfl_xor(st.s, m), __shfl_xor(st.t, m)};
-    // same operand order on both sides, so both get the same bits
-    Stat lo = lane & m ? o : st;
-    join(lo, lane & m ? st : o, c);
-    st = lo;
-  }
+// Highest bit that differs among values with this or and this and (-1: none),
+// and the bits above it, which all of them share.
+__device__ __forceinline__ int first_differing(uint32_t any, uint32_t all) {
+  return any == all ? -1 : 31 - __builtin_clz(any ^ all);
+}
+__device__ __forceinline__ uint32_t common_prefix(uint32_t all, int first) {
+  return first < 0 ? all : all & ~((2u << first) - 1);
 }
 
 // Cuts the list of n keys to its k best, exactly (k < n <= kListCap), and
@@ -129,16 +129,12 @@ __device__ __forceinline__ float cut_list(uint64_t *list, int n, int k) {
     if (lane + 64 * i < n) any |= hi[i], all &= hi[i];
   }
   const int used = (n + 63) / 64;
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    any |= uint32_t(__shfl_xor(int(any), m));
-    all &= uint32_t(__shfl_xor(int(all), m));
-  }
-  const uint32_t spread = __builtin_amdgcn_readfirstlane(any ^ all);
-  uint32_t value = __builtin_amdgcn_readfirstlane(all) &
-                   (spread ? ~((2u << (31 - __builtin_clz(spread))) - 1) : ~0u);
+  any = wave_all<OrU>(any);
+  all = wave_all<AndU>(all);
+  const int first = first_differing(any, all);
+  uint32_t value = common_prefix(all, first);
   int reach = n;                        // entries >= value
-  for (int bit = spread ? 31 - __builtin_clz(spread) : -1; bit >= 0 && reach > k; --bit) {
+  for (int bit = first; bit >= 0 && reach > k; --bit) {
     const uint32_t probe = value | (1u << bit);
     int c = 0;
 #pragma unroll
@@ -171,9 +167,7 @@ __device__ __forceinline__ float cut_list(uint64_t *list, int n, int k) {
     }
     at += __popcll(mask);
   }
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) least = min(least, uint32_t(__shfl_xor(int(least), m)));
-  return from_ordered(least);
+  return from_ordered(wave_all<MinU>(least));
 }
 
 // First tile: a value that at least k of the wave's elements reach, the k-th
@@ -184,14 +178,20 @@ __device__ __forceinline__ float first_threshold(const float cmax[kUnroll], int 
   uint32_t o[kUnroll];
 #pragma unroll
   for (int c = 0; c < kUnroll; ++c) o[c] = ordered(cmax[c]);
-  uint32_t v = 0;
-  for (int bit = 31; bit >= 0; --bit) {
+  uint32_t any = o[0], all = o[0];
+#pragma unroll
+  for (int c = 1; c < kUnroll; ++c) any |= o[c], all &= o[c];
+  any = wave_all<OrU>(any);
+  all = wave_all<AndU>(all);
+  const int first = first_differing(any, all);
+  uint32_t v = common_prefix(all, first);
+  for (int bit = first; bit >= 0; --bit) {
     const uint32_t probe = v | (1u << bit);
     int n = 0;
 #pragma unroll
     for (int c = 0; c < kUnroll; ++c) n += __popcll(__ballot(o[c] >= probe));
     if (n >= k) v = probe;
-    if (n >= k && n <= k + k / 8) break;
+    if (n >= k && n <= k + k / 4 + 1) break;
   }
   const float f = from_ordered(v);
   return f > -INFINITY ? f : -INFINITY;    // also for patterns below -inf
@@ -261,6 +261,10 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
   const int v0 = split * a.seg, v1 = min(v0 + a.seg, a.vocab);
   const float c = a.scale * kLog2e;
 
+  // The first tile is on its way before the given token's logit is asked for.
+  Pack8<T> raw[kUnroll];
+#pragma unroll
+  for (int q = 0; q < kUnroll; ++q) raw[q] = fetch8<E>(l, v0 + q * kChunkElems + 8 * tid, v1);
   const int64_t id = a.ids ? a.ids[row] : -1;
   const bool given = id >= 0 && id < a.vocab;
   const int at = given ? int(id) : 0;
@@ -276,12 +280,13 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
 
   for (int tile = v0; tile < v1; tile += kUnroll * kChunkElems) {
     float x[kUnroll][8], cmax[kUnroll];
-    Pack8<T> raw[kUnroll];
-#pragma unroll
-    for (int q = 0; q < kUnroll; ++q) raw[q] = fetch8<E>(l, tile + q * kChunkElems + 8 * tid, v1);
 #pragma unroll
     for (int q = 0; q < kUnroll; ++q)
       widen8<E>(raw[q], tile + q * kChunkElems + 8 * tid, v1, -INFINITY, x[q]);
+    const int next = tile + kUnroll * kChunkElems;
+    if (next < v1)
+#pragma unroll
+      for (int q = 0; q < kUnroll; ++q) raw[q] = fetch8<E>(l, next + q * kChunkElems + 8 * tid, v1);
     float m = st.m;
 #pragma unroll
     for (int q = 0; q < kUnroll; ++q) {
@@ -377,8 +382,8 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
     }
   }
 
-  join_wave(st, c);
-  if (TOP && n > a.k) {
+  st = join_wave(st, c);
+  if (TOP && n > max(a.k, kUncut)) {
     cut_list(list, n, a.k);
     n = a.k;
   }
@@ -388,12 +393,19 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
     slot_n[wave] = n;
   }
   __syncthreads();
-  st = slot[0];
+  float m_all = slot[0].m;
   ahead = slot_rank[0];
 #pragma unroll
   for (int w = 1; w < kWaves; ++w) {
-    join(st, slot[w], c);
+    m_all = fmaxf(m_all, slot[w].m);
     ahead += slot_rank[w];
+  }
+  st = rescaled(slot[0], m_all, c);
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) {
+    const Stat r = rescaled(slot[w], m_all, c);
+    st.s += r.s;
+    st.t += r.t;
   }
   const bool whole = a.splits == 1;
   RowOut o;
@@ -406,16 +418,19 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
     p[1] = st.s;
     p[2] = st.t;
     p[3] = __int_as_float(ahead);
+    p[4] = lt;
   }
   if (TOP) {
-    // The waves' lists (at most k keys each): a key's place is the number of
+    // The waves' lists (at most 64 keys each): a key's place is the number of
     // larger ones.  Thread w * 64 + i holds entry i of wave w's list.
     const bool mine = lane < slot_n[wave];
     const uint64_t key = mine ? list[lane] : 0;
     int place = 0, total = 0;
+#pragma unroll
     for (int w = 0; w < kWaves; ++w) {
       const int nw = slot_n[w];
       total += nw;
+#pragma unroll 4
       for (int i = 0; i < nw; ++i) place += lists[w * kListCap + i] > key;
     }
     if (whole) {
@@ -434,7 +449,6 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
 // reach; only keys from there on are ranked against each other.
 constexpr int kMaxJoin = 1024;   // splits * k
 constexpr int kMaxSplits = 64;
-template <typename T>
 __global__ void __launch_bounds__(kThreads) score_join_kernel(ScoreArgs a) {
   __shared__ uint64_t keys[kMaxJoin];
   __shared__ uint64_t bound;
@@ -451,12 +465,11 @@ __global__ void __launch_bounds__(kThreads) score_join_kernel(ScoreArgs a) {
   // the splits' statistics, one lane each, joined over the wave
   const float *p = a.part + row * a.splits * kPartWords + min(lane, a.splits - 1) * kPartWords;
   const int64_t id = a.ids ? a.ids[row] : -1;
-  const bool given = id >= 0 && id < a.vocab;
-  const float lt = given ? load_one(static_cast<const T *>(a.logits) + row * a.ld + id) : 0.f;
   Stat st{p[0], p[1], p[2]};
   int ahead = __float_as_int(p[3]);
+  const float lt = p[4];
   if (lane >= a.splits) st = Stat{-3.402823466e38f, 0.f, 0.f}, ahead = 0;
-  join_wave(st, c);
+  st = join_wave(st, c);
   ahead = wave_all<SumI>(ahead);
   const RowOut o = finish_row(a, st, ahead, id, lt);
   if (tid == 0) write_scalars(a, row, o);
@@ -464,12 +477,10 @@ __global__ void __launch_bounds__(kThreads) score_join_kernel(ScoreArgs a) {
   if (tid < 64) {
     uint64_t key = lane < a.splits ? src[lane * a.k + (a.k + a.splits - 1) / a.splits - 1]
                                    : ~uint64_t(0);
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) {
-      const uint64_t other = __shfl_xor(static_cast<unsigned long long>(key), m);
-      key = other < key ? other : key;
-    }
-    if (tid == 0) bound = key, kept = 0;
+    // the least key: its high words first, then the low ones among those
+    const uint32_t hi = wave_all<MinU>(uint32_t(key >> 32));
+    const uint32_t lo = wave_all<MinU>(uint32_t(key >> 32) == hi ? uint32_t(key) : ~0u);
+    if (tid == 0) bound = (uint64_t(hi) << 32) | lo, kept = 0;
   }
   __syncthreads();
 #pragma unroll
@@ -529,7 +540,7 @@ gptq_status score_typed(const ScoreArgs &a, int64_t rows, hipStream_t s) {
     default: GPTQ_TRY((score_ends<T, kShort>(a, rows, s)));
   }
   if (a.splits == 1) return GPTQ_OK;
-  return launch("token_logprobs_join", score_join_kernel<T>, dim3(uint32_t(rows)), dim3(kThreads), 0,
+  return launch("token_logprobs_join", score_join_kernel, dim3(uint32_t(rows)), dim3(kThreads), 0,
                 s, a);
 }
 
