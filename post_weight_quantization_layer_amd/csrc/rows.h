@@ -123,9 +123,9 @@ __device__ __forceinline__ void widen8(const Pack8<T> &k, int e0, int d, float f
 #pragma unroll
   for (int j = 0; j < 8; ++j) out[j] = k.at(j);
   if (E == kWhole) {                   // all eight or none
-    if (n <= 0) {
+    if (__ballot(n <= 0)) {            // a branch of the whole wave, rarely taken
 #pragma unroll
-      for (int j = 0; j < 8; ++j) out[j] = fill;
+      for (int j = 0; j < 8; ++j) out[j] = n <= 0 ? fill : out[j];
     }
     return;
   }

@@ -8,13 +8,15 @@
 // ln s and the entropy is ln s - ln 2 t / s.  c l - M is one fused operation,
 // exact up to its last rounding because M, not c m, is the reference.
 //
-// Alternatives: each wave keeps a short list of candidates in LDS, every
-// logit above a threshold that k logits of the wave are known to reach.  The
-// first tile's threshold is the k-th largest of the wave's 256 maxima over 8
-// logits; whenever the list grows past a few k it is cut to its k best,
-// whose smallest is the new threshold.  So after the first tile almost every
-// tile costs one comparison per lane.  All selections go by (value, lower
-// index), so the result does not depend on the order of the work.
+// Alternatives: the pass keeps each lane's maximum over groups of tiles, in
+// LDS.  After it, the k-th largest of the 256 lanes' own maxima is a threshold
+// that k logits reach and few others, and only the tiles whose group reaches it
+// are read again (from cache, about k of them), into a short list per wave;
+// where a list grows past a few k it is cut to its k best, whose smallest is
+// the new threshold.  Candidates listed during the pass instead, each wave
+// against its own rising threshold, cost as much as the pass itself.  All
+// selections go by (value, lower index), so the result does not depend on the
+// order of the work.
 #include <algorithm>
 
 #include "rows.h"
@@ -26,9 +28,12 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kChunkElems = 8 * kThreads;   // elements a workgroup takes per chunk
 constexpr int kMaxTop = 64;
+constexpr int kGroups = 32;                 // groups of tiles with a maximum of their own
 constexpr int kUncut = 24;                  // shorter lists are not cut before the last step
-// A wave's list takes a whole chunk (512) on top of k cut entries.
-constexpr int kListCap = 512 + kMaxTop;
+// A wave's list is cut to k once it is longer than 2 k + 32, before the next
+// entry is added; so it takes a chunk (512) on top of that.
+constexpr int kListSlack = 32;
+constexpr int kListCap = 512 + 2 * kMaxTop + kListSlack;
 
 struct ScoreArgs {
   const void *logits;
@@ -117,7 +122,7 @@ __device__ __forceinline__ uint32_t common_prefix(uint32_t all, int first) {
 // if more than k entries reach it, their lowest indices are searched the same
 // way.  One wave; the list is in its LDS.
 __device__ __forceinline__ float cut_list(uint64_t *list, int n, int k) {
-  constexpr int kPer = kListCap / 64;   // 9
+  constexpr int kPer = (kListCap + 63) / 64;   // 11
   const int lane = threadIdx.x & 63;
   uint32_t hi[kPer], lo[kPer];
   uint32_t any = 0, all = ~0u;
@@ -250,7 +255,10 @@ __device__ __forceinline__ float load_one(const f16_t *p) { return widen(*p); }
 // Workgroup (row, split): the row's elements [split seg, split seg + seg).
 template <typename T, Ends E, int kUnroll, bool TOP>
 __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
+  constexpr bool kLater = TOP && kUnroll > 1;   // alternatives in a second step
+  constexpr int kTile = kUnroll * kChunkElems;
   __shared__ uint64_t lists[TOP ? kWaves * kListCap : 1];
+  __shared__ float lane_max[kLater ? kThreads : 1];
   __shared__ Stat slot[kWaves];
   __shared__ int slot_rank[kWaves], slot_n[kWaves];
   const int64_t row = blockIdx.x / a.splits;
@@ -273,43 +281,104 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
 
   Stat st{-3.402823466e38f, 0.f, 0.f};
   int ahead = 0;                   // the wave's count
+  bool masked = false;             // whether -infinity has been seen (by the wave)
   uint64_t *list = lists + (TOP ? wave * kListCap : 0);
+  // The group maxima of a wave lie where its list will be.
+  static_assert(kGroups * 64 * 2 <= kListCap * 8, "");
+  uint16_t *group_max = reinterpret_cast<uint16_t *>(list) + lane;
   int n = 0;                       // list length (wave-uniform)
   float thr = -INFINITY;           // candidates are > thr
-  const int limit = 2 * a.k + 32;  // list length that is cut after a tile
+  const int limit = 2 * a.k + kListSlack;
 
-  for (int tile = v0; tile < v1; tile += kUnroll * kChunkElems) {
-    float x[kUnroll][8], cmax[kUnroll];
-#pragma unroll
-    for (int q = 0; q < kUnroll; ++q)
-      widen8<E>(raw[q], tile + q * kChunkElems + 8 * tid, v1, -INFINITY, x[q]);
-    const int next = tile + kUnroll * kChunkElems;
-    if (next < v1)
-#pragma unroll
-      for (int q = 0; q < kUnroll; ++q) raw[q] = fetch8<E>(l, next + q * kChunkElems + 8 * tid, v1);
-    float m = st.m;
+  // A tile's values and the maximum of each 8.
+  float x[kUnroll][8], cmax[kUnroll];
+  auto widen_tile = [&](int tile) {
 #pragma unroll
     for (int q = 0; q < kUnroll; ++q) {
-      cmax[q] = x[q][0];
-#pragma unroll
-      for (int j = 1; j < 8; ++j) cmax[q] = fmaxf(cmax[q], x[q][j]);
-      m = fmaxf(m, cmax[q]);
+      widen8<E>(raw[q], tile + q * kChunkElems + 8 * tid, v1, -INFINITY, x[q]);
+      // three at a time
+      const float h = fmaxf(fmaxf(x[q][0], x[q][1]), x[q][2]);
+      const float i = fmaxf(fmaxf(h, x[q][3]), x[q][4]);
+      cmax[q] = fmaxf(fmaxf(fmaxf(i, x[q][5]), x[q][6]), x[q][7]);
     }
+  };
+  auto fetch_tile = [&](int tile) {
+#pragma unroll
+    for (int q = 0; q < kUnroll; ++q) raw[q] = fetch8<E>(l, tile + q * kChunkElems + 8 * tid, v1);
+  };
+  // Adds a tile's entries above the threshold to the list.  Tiles come in
+  // index order, so after a cut entries that only equal the threshold lose
+  // against the k that reach it.
+  auto list_tile = [&](int tile) {
+#pragma unroll
+    for (int q = 0; q < kUnroll; ++q) {
+      if (!__ballot(cmax[q] > thr)) continue;
+      if (n > limit) {                 // then a whole chunk fits
+        thr = fmaxf(thr, cut_list(list, n, a.k));
+        n = a.k;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool take = x[q][j] > thr;
+        const uint64_t mask = __ballot(take);
+        if (!mask) continue;           // most of the eight: nothing to add
+        if (take)
+          list[n + __popcll(mask & ((uint64_t(1) << lane) - 1))] =
+              make_key(x[q][j], tile + q * kChunkElems + 8 * tid + j);
+        n += __popcll(mask);
+      }
+    }
+  };
+  const int per_group = ((v1 - v0 + kTile - 1) / kTile + kGroups - 1) / kGroups;   // tiles
+  float group = -INFINITY;             // the lane's maximum over the current group
+  int in_group = 0, groups = 0;
+
+  for (int tile = v0; tile < v1; tile += kTile) {
+    widen_tile(tile);
+    if (tile + kTile < v1) fetch_tile(tile + kTile);
+    float m = st.m;
+#pragma unroll
+    for (int q = 0; q < kUnroll; ++q) m = fmaxf(m, cmax[q]);
     const float M = reference(m, c);
     if (!__ballot(!(fabsf(M) < kLarge))) {
       // (a lane whose elements were all -infinity so far has s = t = 0)
       const float dm = fmaxf(reference(st.m, c) - M, -200.f), f = __builtin_amdgcn_exp2f(dm);
       st.t = f * (st.t + dm * st.s);
       st.s *= f;
+      if (!masked) {
+        const float t = st.t;
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i)
+        for (int i = 0; i < kUnroll; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float d = __builtin_fmaf(x[i][j], c, -M);
-          const float e = __builtin_amdgcn_exp2f(d);
-          st.s += e;
-          st.t = __builtin_fmaf(fmaxf(d, -3e38f), e, st.t);   // -inf: 0
+          for (int j = 0; j < 8; ++j) {
+            const float d = __builtin_fmaf(x[i][j], c, -M);
+            const float e = __builtin_amdgcn_exp2f(d);
+            st.s += e;
+            st.t = __builtin_fmaf(d, e, st.t);
+          }
+        // -infinity times 0: such a row takes the other form from here on
+        masked = __ballot(!(st.t == st.t)) != 0;
+        if (masked) {
+          st.t = t;
+#pragma unroll
+          for (int i = 0; i < kUnroll; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float d = __builtin_fmaf(x[i][j], c, -M);
+              st.t = __builtin_fmaf(fmaxf(d, -3e38f), __builtin_amdgcn_exp2f(d), st.t);
+            }
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float d = __builtin_fmaf(x[i][j], c, -M);
+            const float e = __builtin_amdgcn_exp2f(d);
+            st.s += e;
+            st.t = __builtin_fmaf(fmaxf(d, -3e38f), e, st.t);   // -inf: 0
+          }
+      }
     } else {
       // Some lane has only -infinity or huge values so far.
       const float dm = exponent(st.m, m, c), f = exp2f(dm);
@@ -336,48 +405,58 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) ahead += __popcll(__ballot(x[q][j] > from));
         const bool has_given = !before && e0 < at && e0 < v1;
-        const bool masked = before && e0 < v1 && lt == -INFINITY;   // all eight are >= -inf
-        if (__ballot(has_given || masked)) {
-          ahead += 8 * __popcll(__ballot(masked));
+        const bool below_given = before && e0 < v1 && lt == -INFINITY;   // all eight are >= -inf
+        if (__ballot(has_given || below_given)) {
+          ahead += 8 * __popcll(__ballot(below_given));
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             ahead += __popcll(__ballot(has_given && e0 + j < at && x[q][j] == lt));
         }
       }
     }
-    if (TOP) {
-      float strict = thr;
+    if (kLater) {
+#pragma unroll
+      for (int q = 0; q < kUnroll; ++q) group = fmaxf(group, cmax[q]);
+      if (++in_group == per_group || tile + kTile >= v1) {
+        // the upper half of the ordered form, rounded up
+        const uint32_t o = ordered(group);
+        group_max[groups * 64] = uint16_t(min((o >> 16) + ((o & 0xffffu) != 0), 0xffffu));
+        ++groups;
+        in_group = 0;
+        group = -INFINITY;
+      }
+    } else if (TOP) {
+      float strict = -INFINITY;
       if (tile == v0) {
         strict = first_threshold<kUnroll>(cmax, a.k);
         if (strict > -INFINITY) thr = below(strict);
       }
+      list_tile(tile);
+      thr = fmaxf(thr, strict);        // its k entries came in this tile
+    }
+  }
+  if (kLater) {
+    // The k-th largest of the 256 lanes' maxima is reached by k elements of the
+    // row, and few others: only groups that reach it are read again.
+    lane_max[tid] = st.s == 0.f ? -INFINITY : st.m;
+    __syncthreads();
+    float most[kWaves];
 #pragma unroll
-      for (int q = 0; q < kUnroll; ++q) {
-        if (!__ballot(cmax[q] > thr)) continue;
-        int add = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) add += __popcll(__ballot(x[q][j] > thr));
-        if (n + add > kListCap) {      // wave-uniform; then n is k and a chunk fits
-          strict = cut_list(list, n, a.k);
-          thr = fmaxf(thr, strict);
-          n = a.k;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const bool take = x[q][j] > thr;
-          const uint64_t mask = __ballot(take);
-          if (take)
-            list[n + __popcll(mask & ((uint64_t(1) << lane) - 1))] =
-                make_key(x[q][j], tile + q * kChunkElems + 8 * tid + j);
-          n += __popcll(mask);
-        }
-      }
-      // Later entries that only equal the threshold have higher indices than
-      // the k entries that reach it.
-      thr = fmaxf(thr, strict);
-      if (n > limit) {
-        thr = fmaxf(thr, cut_list(list, n, a.k));
-        n = a.k;
+    for (int w = 0; w < kWaves; ++w) most[w] = lane_max[w * 64 + lane];
+    const float reached = first_threshold<kWaves>(most, a.k);
+    if (reached > -INFINITY) thr = below(reached);
+    const uint32_t bar = ordered(thr) >> 16;
+    uint32_t todo = 0;                 // groups, a bit each
+    for (int g = 0; g < groups; ++g)
+      if (__ballot(group_max[g * 64] >= bar)) todo |= 1u << g;
+    while (todo) {
+      const int g = __builtin_ctz(todo);
+      todo &= todo - 1;
+      const int first = v0 + g * per_group * kTile, last = min(first + per_group * kTile, v1);
+      for (int tile = first; tile < last; tile += kTile) {
+        fetch_tile(tile);
+        widen_tile(tile);
+        list_tile(tile);
       }
     }
   }
@@ -519,8 +598,9 @@ size_t score_ws(int64_t rows, int64_t vocab, int32_t k, int cus) {
          align256(size_t(rows) * p.splits * size_t(k) * sizeof(uint64_t));
 }
 
-// One chunk per tile where a workgroup has few of them (single tokens), four
-// otherwise, whose loads are then in flight together.
+// One chunk per tile where a workgroup has few of them (single tokens), two
+// otherwise (four cost a wave's registers their company: 4096 x 128000 with 20
+// alternatives took 399 us with four, 308 with two).
 template <typename T, Ends E, int kUnroll>
 gptq_status score_tiles(const ScoreArgs &a, int64_t rows, hipStream_t s) {
   const dim3 grid(uint32_t(rows * a.splits)), block(kThreads);
@@ -530,7 +610,7 @@ gptq_status score_tiles(const ScoreArgs &a, int64_t rows, hipStream_t s) {
 template <typename T, Ends E>
 gptq_status score_ends(const ScoreArgs &a, int64_t rows, hipStream_t s) {
   return a.seg <= 2 * kChunkElems ? score_tiles<T, E, 1>(a, rows, s)
-                                  : score_tiles<T, E, 4>(a, rows, s);
+                                  : score_tiles<T, E, 2>(a, rows, s);
 }
 template <typename T>
 gptq_status score_typed(const ScoreArgs &a, int64_t rows, hipStream_t s) {
