@@ -27,19 +27,23 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kChunkElems = 8 * kThreads;   // elements a workgroup takes per chunk
+// Chunks per tile, whose loads are in flight together (with four, a wave's
+// registers leave room for fewer waves: 4096 x 128000 399 us against 308).
+constexpr int kUnroll = 2;
+constexpr int kTile = kUnroll * kChunkElems;
 constexpr int kMaxTop = 64;
 constexpr int kGroups = 32;                 // groups of tiles with a maximum of their own
-constexpr int kUncut = 24;                  // shorter lists are not cut before the last step
+constexpr int kUncut = 64;                  // shorter lists are not cut before the last step
 // A wave's list is cut to k once it is longer than 2 k + 32, before the next
 // entry is added; so it takes a chunk (512) on top of that.
 constexpr int kListSlack = 32;
-constexpr int kListCap = 512 + 2 * kMaxTop + kListSlack;
+constexpr int kListCap = 512 + 2 * kMaxTop + kListSlack + 16;   // 16: zeros after the last
 
 struct ScoreArgs {
   const void *logits;
   const int64_t *ids;
   int64_t ld;
-  int vocab, k, splits, seg;    // seg: elements per split (a multiple of kChunkElems)
+  int vocab, k, splits, seg;    // seg: elements per split (a multiple of kTile)
   float scale;
   float *logprob;
   int *rank;
@@ -143,8 +147,10 @@ __device__ __forceinline__ float cut_list(uint64_t *list, int n, int k) {
     const uint32_t probe = value | (1u << bit);
     int c = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i < used) c += __popcll(__ballot(hi[i] >= probe));
+    for (int i = 0; i < kPer; ++i) {
+      if (i >= used) break;
+      c += __popcll(__ballot(hi[i] >= probe));
+    }
     if (c >= k) value = probe, reach = c;
   }
   uint32_t low = 0;                     // of those equal to value: keep lo >= low
@@ -153,8 +159,10 @@ __device__ __forceinline__ float cut_list(uint64_t *list, int n, int k) {
       const uint32_t probe = low | (1u << bit);
       int c = 0;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i < used) c += __popcll(__ballot(hi[i] > value || (hi[i] == value && lo[i] >= probe)));
+      for (int i = 0; i < kPer; ++i) {
+        if (i >= used) break;
+        c += __popcll(__ballot(hi[i] > value || (hi[i] == value && lo[i] >= probe)));
+      }
       if (c >= k) low = probe;
       if (c == k) break;
     }
@@ -175,17 +183,29 @@ __device__ __forceinline__ float cut_list(uint64_t *list, int n, int k) {
   return from_ordered(wave_all<MinU>(least));
 }
 
-// First tile: a value that at least k of the wave's elements reach, the k-th
-// largest of its maxima over 8 elements or a little below (-inf if fewer than
-// k are above).
-template <int kUnroll>
-__device__ __forceinline__ float first_threshold(const float cmax[kUnroll], int k) {
-  uint32_t o[kUnroll];
+// How many of kBatch keys in LDS are above `key`; the reads are in flight
+// together.
+constexpr int kBatch = 16;
+__device__ __forceinline__ int count_above(const uint64_t *keys, uint64_t key) {
+  uint64_t e[kBatch];
 #pragma unroll
-  for (int c = 0; c < kUnroll; ++c) o[c] = ordered(cmax[c]);
+  for (int i = 0; i < kBatch; ++i) e[i] = keys[i];
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) n += e[i] > key;
+  return n;
+}
+
+// A value that at least k elements of the row's part reach: the k-th largest of
+// the 256 lanes' maxima (four to a lane here) or a little below; -inf if fewer
+// than k are above that.
+__device__ __forceinline__ float reached_by(const float most[kWaves], int k) {
+  uint32_t o[kWaves];
+#pragma unroll
+  for (int c = 0; c < kWaves; ++c) o[c] = ordered(most[c]);
   uint32_t any = o[0], all = o[0];
 #pragma unroll
-  for (int c = 1; c < kUnroll; ++c) any |= o[c], all &= o[c];
+  for (int c = 1; c < kWaves; ++c) any |= o[c], all &= o[c];
   any = wave_all<OrU>(any);
   all = wave_all<AndU>(all);
   const int first = first_differing(any, all);
@@ -194,7 +214,7 @@ __device__ __forceinline__ float first_threshold(const float cmax[kUnroll], int 
     const uint32_t probe = v | (1u << bit);
     int n = 0;
 #pragma unroll
-    for (int c = 0; c < kUnroll; ++c) n += __popcll(__ballot(o[c] >= probe));
+    for (int c = 0; c < kWaves; ++c) n += __popcll(__ballot(o[c] >= probe));
     if (n >= k) v = probe;
     if (n >= k && n <= k + k / 4 + 1) break;
   }
@@ -253,12 +273,10 @@ __device__ __forceinline__ float load_one(const bf16_t *p) { return widen(*p); }
 __device__ __forceinline__ float load_one(const f16_t *p) { return widen(*p); }
 
 // Workgroup (row, split): the row's elements [split seg, split seg + seg).
-template <typename T, Ends E, int kUnroll, bool TOP>
+template <typename T, Ends E, bool TOP>
 __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
-  constexpr bool kLater = TOP && kUnroll > 1;   // alternatives in a second step
-  constexpr int kTile = kUnroll * kChunkElems;
   __shared__ uint64_t lists[TOP ? kWaves * kListCap : 1];
-  __shared__ float lane_max[kLater ? kThreads : 1];
+  __shared__ float lane_max[TOP ? kThreads : 1];
   __shared__ Stat slot[kWaves];
   __shared__ int slot_rank[kWaves], slot_n[kWaves];
   const int64_t row = blockIdx.x / a.splits;
@@ -414,7 +432,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
         }
       }
     }
-    if (kLater) {
+    if (TOP) {
 #pragma unroll
       for (int q = 0; q < kUnroll; ++q) group = fmaxf(group, cmax[q]);
       if (++in_group == per_group || tile + kTile >= v1) {
@@ -425,17 +443,9 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
         in_group = 0;
         group = -INFINITY;
       }
-    } else if (TOP) {
-      float strict = -INFINITY;
-      if (tile == v0) {
-        strict = first_threshold<kUnroll>(cmax, a.k);
-        if (strict > -INFINITY) thr = below(strict);
-      }
-      list_tile(tile);
-      thr = fmaxf(thr, strict);        // its k entries came in this tile
     }
   }
-  if (kLater) {
+  if (TOP) {
     // The k-th largest of the 256 lanes' maxima is reached by k elements of the
     // row, and few others: only groups that reach it are read again.
     lane_max[tid] = st.s == 0.f ? -INFINITY : st.m;
@@ -443,7 +453,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
     float most[kWaves];
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) most[w] = lane_max[w * 64 + lane];
-    const float reached = first_threshold<kWaves>(most, a.k);
+    const float reached = reached_by(most, a.k);
     if (reached > -INFINITY) thr = below(reached);
     const uint32_t bar = ordered(thr) >> 16;
     uint32_t todo = 0;                 // groups, a bit each
@@ -454,18 +464,21 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
       todo &= todo - 1;
       const int first = v0 + g * per_group * kTile, last = min(first + per_group * kTile, v1);
       for (int tile = first; tile < last; tile += kTile) {
-        fetch_tile(tile);
-        widen_tile(tile);
+        if (v1 - v0 > kTile) {         // a single tile is still there
+          fetch_tile(tile);
+          widen_tile(tile);
+        }
         list_tile(tile);
       }
     }
   }
 
   st = join_wave(st, c);
-  if (TOP && n > max(a.k, kUncut)) {
+  if (TOP && n > kUncut) {
     cut_list(list, n, a.k);
     n = a.k;
   }
+  if (TOP && lane < kBatch) list[n + lane] = 0;
   if (lane == 0) {
     slot[wave] = st;
     slot_rank[wave] = ahead;
@@ -500,17 +513,16 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
     p[4] = lt;
   }
   if (TOP) {
-    // The waves' lists (at most 64 keys each): a key's place is the number of
-    // larger ones.  Thread w * 64 + i holds entry i of wave w's list.
+    // The waves' lists (at most 64 keys each, zeros up to a multiple of
+    // kBatch): a key's place is the number of larger ones, counted a batch of
+    // LDS reads at a time.  Thread w * 64 + i holds entry i of wave w's list.
     const bool mine = lane < slot_n[wave];
     const uint64_t key = mine ? list[lane] : 0;
     int place = 0, total = 0;
-#pragma unroll
     for (int w = 0; w < kWaves; ++w) {
       const int nw = slot_n[w];
       total += nw;
-#pragma unroll 4
-      for (int i = 0; i < nw; ++i) place += lists[w * kListCap + i] > key;
+      for (int i = 0; i < nw; i += kBatch) place += count_above(lists + w * kListCap + i, key);
     }
     if (whole) {
       if (mine && place < a.k) write_top(a, row, place, o, true, key);
@@ -529,7 +541,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
 constexpr int kMaxJoin = 1024;   // splits * k
 constexpr int kMaxSplits = 64;
 __global__ void __launch_bounds__(kThreads) score_join_kernel(ScoreArgs a) {
-  __shared__ uint64_t keys[kMaxJoin];
+  __shared__ uint64_t keys[kMaxJoin + kBatch];
   __shared__ uint64_t bound;
   __shared__ int kept;
   const int64_t row = blockIdx.x;
@@ -567,26 +579,29 @@ __global__ void __launch_bounds__(kThreads) score_join_kernel(ScoreArgs a) {
     if (mine[i] != 0 && mine[i] >= bound) keys[atomicAdd(&kept, 1)] = mine[i];   // in any order
   __syncthreads();
   const int total = kept;
+  if (tid < kBatch) keys[total + tid] = 0;
+  __syncthreads();
   for (int at = tid; at < total; at += kThreads) {
     const uint64_t key = keys[at];
     int place = 0;
-    for (int i = 0; i < total; ++i) place += keys[i] > key;
+    for (int i = 0; i < total; i += kBatch) place += count_above(keys + i, key);
     if (place < a.k) write_top(a, row, place, o, true, key);
   }
   if (tid >= total && tid < a.k) write_top(a, row, tid, o, false, 0);
 }
 
-// A row is split over workgroups until the launch has about four of them
-// per compute unit; a split takes whole chunks.
+// A row is split over workgroups, by whole tiles, until there is about one of
+// them per compute unit (16 x 128000 with 20 alternatives: 13.4 us, 17.1 with
+// four per unit, whose join has more to rank).
 struct ScorePlan {
   int splits, seg;
 };
 ScorePlan score_plan(int64_t rows, int64_t vocab, int32_t k, int cus) {
-  const int64_t chunks = cdiv(vocab, kChunkElems);
+  const int64_t tiles = cdiv(vocab, kTile);
   const int64_t most = std::min<int64_t>(kMaxSplits, kMaxJoin / std::max(k, 1));
-  const int64_t want = std::min<int64_t>({chunks, cdiv(4 * int64_t(cus), rows), most});
-  const int64_t per = cdiv(chunks, want);
-  return {int(cdiv(chunks, per)), int(per * kChunkElems)};
+  const int64_t want = std::min<int64_t>({tiles, cdiv(cus, rows), most});
+  const int64_t per = cdiv(tiles, want);
+  return {int(cdiv(tiles, per)), int(per * kTile)};
 }
 
 constexpr size_t kPartBytes = kPartWords * sizeof(float);
@@ -598,19 +613,11 @@ size_t score_ws(int64_t rows, int64_t vocab, int32_t k, int cus) {
          align256(size_t(rows) * p.splits * size_t(k) * sizeof(uint64_t));
 }
 
-// One chunk per tile where a workgroup has few of them (single tokens), two
-// otherwise (four cost a wave's registers their company: 4096 x 128000 with 20
-// alternatives took 399 us with four, 308 with two).
-template <typename T, Ends E, int kUnroll>
-gptq_status score_tiles(const ScoreArgs &a, int64_t rows, hipStream_t s) {
-  const dim3 grid(uint32_t(rows * a.splits)), block(kThreads);
-  return a.k ? launch("token_logprobs", score_kernel<T, E, kUnroll, true>, grid, block, 0, s, a)
-             : launch("token_logprobs", score_kernel<T, E, kUnroll, false>, grid, block, 0, s, a);
-}
 template <typename T, Ends E>
 gptq_status score_ends(const ScoreArgs &a, int64_t rows, hipStream_t s) {
-  return a.seg <= 2 * kChunkElems ? score_tiles<T, E, 1>(a, rows, s)
-                                  : score_tiles<T, E, 2>(a, rows, s);
+  const dim3 grid(uint32_t(rows * a.splits)), block(kThreads);
+  return a.k ? launch("token_logprobs", score_kernel<T, E, true>, grid, block, 0, s, a)
+             : launch("token_logprobs", score_kernel<T, E, false>, grid, block, 0, s, a);
 }
 template <typename T>
 gptq_status score_typed(const ScoreArgs &a, int64_t rows, hipStream_t s) {
