@@ -35,17 +35,21 @@ def _bf16_buffer(rows: int, n: int, device) -> torch.Tensor:
 
 
 class GatedMLPCalibrator:
-    """Buffers for one gated MLP block (d -> d_ff -> d) on one device."""
+    """Buffers for one gated MLP block (d -> d_ff -> d) on one device.
 
-    def __init__(self, d: int, d_ff: int, *, bits: int, group: int, block: int,
+    ``group`` None: one group per row in each layer, the form the 8-bit product
+    (W8A8Linear) takes."""
+
+    def __init__(self, d: int, d_ff: int, *, bits: int, group: int | None, block: int,
                  act_order: bool, percdamp: float = 0.01, grid: str = "affine",
                  search: bool = False, device="cuda"):
-        kw = dict(bits=bits, group=group, block=block, act_order=act_order,
-                  percdamp=percdamp, grid=grid, device=device, search=search)
+        kw = dict(bits=bits, block=block, act_order=act_order, percdamp=percdamp, grid=grid,
+                  device=device, search=search)
         self.d, self.d_ff = d, d_ff
         self.device = torch.device(device)
-        self.gate_up = GptqLayer(d_ff, d, **kw)    # one Hessian for gate and up
-        self.down = GptqLayer(d, d_ff, **kw)
+        # one Hessian for gate and up
+        self.gate_up = GptqLayer(d_ff, d, group=d if group is None else group, **kw)
+        self.down = GptqLayer(d, d_ff, group=d_ff if group is None else group, **kw)
 
     def run(self, W_gate: torch.Tensor, W_up: torch.Tensor, W_down: torch.Tensor,
             x_chunks, stream=None) -> GatedMLPResult:
