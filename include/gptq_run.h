@@ -208,7 +208,7 @@ size_t gptq_token_logprobs_ws_bytes(int64_t rows, int64_t vocab, int32_t top_k);
  *  logits  rows x vocab of dtype, row stride ld.  1 <= vocab <= 2^24, rows <=
  *          2^24.
  *  ids     rows int64, or NULL (then logprob and rank are not written).
- *  scale   finite, > 0: the inverse temperature.
+ *  scale   the inverse temperature, in [1e-30, 1e30].
  *  top_k   0..64 and at most vocab.
  *  logprob, rank, entropy  rows float / int32 / float, each may be NULL.
  *  top_ids, top_logprobs   rows x top_k int32 / float, not NULL for top_k >

@@ -459,17 +459,31 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
     uint32_t todo = 0;                 // groups, a bit each
     for (int g = 0; g < groups; ++g)
       if (__ballot(group_max[g * 64] >= bar)) todo |= 1u << g;
-    while (todo) {
-      const int g = __builtin_ctz(todo);
-      todo &= todo - 1;
-      const int first = v0 + g * per_group * kTile, last = min(first + per_group * kTile, v1);
-      for (int tile = first; tile < last; tile += kTile) {
-        if (v1 - v0 > kTile) {         // a single tile is still there
-          fetch_tile(tile);
-          widen_tile(tile);
-        }
-        list_tile(tile);
+    // Tiles of those groups, the next one's loads in flight; a part's only tile
+    // is still there.
+    const bool single = v1 - v0 <= kTile;
+    int left = 0, tile = v1;
+    auto advance = [&]() {
+      if (left > 0) {
+        --left;
+        tile += kTile;
+      } else if (todo) {
+        tile = v0 + __builtin_ctz(todo) * per_group * kTile;
+        todo &= todo - 1;
+        left = per_group - 1;
+      } else {
+        tile = v1;
       }
+      return tile < v1;                // only the last group can end past v1
+    };
+    bool more = advance();
+    if (more && !single) fetch_tile(tile);
+    while (more) {
+      const int now = tile;
+      if (!single) widen_tile(now);
+      more = advance();
+      if (more) fetch_tile(tile);
+      list_tile(now);
     }
   }
 
@@ -659,8 +673,8 @@ gptq_status gptq_token_logprobs(const void *logits, int32_t dtype, int64_t rows,
                   "rows and vocab must be in [0, 2^24] x [1, 2^24], top_k in [0, min(64, vocab)]");
     if (!is_float_type(dtype))
       return fail(GPTQ_ERR_INVALID_ARG, "the logits' type must be F32, BF16 or F16");
-    if (!(scale > 0.f) || !(scale < HUGE_VALF))
-      return fail(GPTQ_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (!(scale >= 1e-30f) || !(scale <= 1e30f))
+      return fail(GPTQ_ERR_INVALID_ARG, "scale must be in [1e-30, 1e30]");
     if (rows == 0) return GPTQ_OK;
     if (!logits) return fail(GPTQ_ERR_INVALID_ARG, "logits must not be NULL");
     if (!aligned_to(logits, type_bytes(dtype)) || !aligned_to(ids, 8))

@@ -132,7 +132,7 @@ def test_norm_block_refuses(change, word):
     (dict(logits=None), BAD, "logits"), (dict(logits=A + 1), BAD, "aligned"),
     (dict(ids=A + 4), BAD, "aligned"), (dict(dtype=8), BAD, "type"), (dict(rows=-1), BAD, "rows"),
     (dict(vocab=0), BAD, "vocab"), (dict(vocab=(1 << 24) + 1), BAD, "vocab"), (dict(ld=999), BAD, "ld"),
-    (dict(scale=0.0), BAD, "scale"), (dict(scale=float("inf")), BAD, "scale"),
+    (dict(scale=0.0), BAD, "scale"), (dict(scale=1e31), BAD, "scale"), (dict(scale=float("inf")), BAD, "scale"),
     (dict(scale=float("nan")), BAD, "scale"), (dict(k=65), BAD, "top_k"),
     (dict(k=20, vocab=10, ld=10), BAD, "top_k"), (dict(top_ids=None), BAD, "top_ids"),
     (dict(ids=None), BAD, "ids"), (dict(entropy=A + 2), BAD, "aligned"),
