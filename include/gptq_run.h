@@ -23,7 +23,8 @@
  * Token-major layout: activations are tokens x features, row-major, with a
  * row stride (ld) in elements.  Unless stated, a float buffer needs only its
  * element's alignment, and any stride of at least the row's length.
- * Token counts of zero are no-ops.  Everything is asynchronous on `stream`.
+ * Token counts of zero are no-ops; they go up to 2^21 where nothing else is
+ * stated.  Everything is asynchronous on `stream`.
  * Each result depends on its own row's inputs alone and comes out as the
  * same bits on every call with the same sizes.
  */
@@ -85,7 +86,7 @@ typedef struct {
 } gptq_w8a8_layer;
 
 /* Bytes of device memory a prepared layer needs (0 on invalid sizes: rows in
- * [1, 2^24], cols in [1, 65536]). */
+ * [1, 2^24], cols in [1, 65536], rows_pad * k_pad <= 2^35). */
 size_t gptq_w8a8_layer_bytes(int64_t rows, int64_t cols);
 
 /*
@@ -206,7 +207,7 @@ size_t gptq_token_logprobs_ws_bytes(int64_t rows, int64_t vocab, int32_t top_k);
 
 /*
  *  logits  rows x vocab of dtype, row stride ld.  1 <= vocab <= 2^24, rows <=
- *          2^24.
+ *          2^23.
  *  ids     rows int64, or NULL (then logprob and rank are not written).
  *  scale   the inverse temperature, in [1e-30, 1e30].
  *  top_k   0..64 and at most vocab.

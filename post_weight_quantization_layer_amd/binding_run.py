@@ -189,7 +189,7 @@ def gptq_w8a8_layer_bytes(rows: int, cols: int) -> int:
     n = lib().gptq_w8a8_layer_bytes(rows, cols)
     if n == 0:
         raise B.GptqError(B.GPTQ_ERR_INVALID_ARG,
-                          "rows and cols must be in [1, 2^24] x [1, 65536]")
+                          "rows and cols must be in [1, 2^24] x [1, 65536], padded at most 2^35")
     return n
 
 

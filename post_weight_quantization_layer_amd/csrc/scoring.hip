@@ -645,7 +645,8 @@ gptq_status score_typed(const ScoreArgs &a, int64_t rows, hipStream_t s) {
                 s, a);
 }
 
-constexpr int64_t kMaxVocab = int64_t(1) << 24, kMaxScoreRows = int64_t(1) << 24;
+// A launch has at most 2^32 threads, 256 of them per row here.
+constexpr int64_t kMaxVocab = int64_t(1) << 24, kMaxScoreRows = int64_t(1) << 23;
 bool valid_score(int64_t rows, int64_t vocab, int32_t k) {
   return rows >= 0 && rows <= kMaxScoreRows && vocab >= 1 && vocab <= kMaxVocab && k >= 0 &&
          k <= kMaxTop && k <= vocab;
@@ -670,7 +671,7 @@ gptq_status gptq_token_logprobs(const void *logits, int32_t dtype, int64_t rows,
   return guarded([&]() -> gptq_status {
     if (!valid_score(rows, vocab, top_k))
       return fail(GPTQ_ERR_INVALID_ARG,
-                  "rows and vocab must be in [0, 2^24] x [1, 2^24], top_k in [0, min(64, vocab)]");
+                  "rows and vocab must be in [0, 2^23] x [1, 2^24], top_k in [0, min(64, vocab)]");
     if (!is_float_type(dtype))
       return fail(GPTQ_ERR_INVALID_ARG, "the logits' type must be F32, BF16 or F16");
     if (!(scale >= 1e-30f) || !(scale <= 1e30f))

@@ -423,7 +423,8 @@ gptq_status check_codes(const int8_t *codes, int64_t ld_codes, int64_t cols, con
   return GPTQ_OK;
 }
 
-constexpr int64_t kMaxTokens = int64_t(1) << 24;
+// A launch has at most 2^32 threads, 1024 of them per row here.
+constexpr int64_t kMaxTokens = int64_t(1) << 21;
 
 }  // namespace
 
@@ -442,7 +443,7 @@ gptq_status check_activations(const void *x, int32_t dtype, int64_t tokens, int6
   if (!is_float_type(dtype))
     return fail(GPTQ_ERR_INVALID_ARG, w + "'s type must be F32, BF16 or F16");
   if (tokens < 0 || tokens > kMaxTokens)
-    return fail(GPTQ_ERR_INVALID_ARG, "tokens must be in [0, 2^24]");
+    return fail(GPTQ_ERR_INVALID_ARG, "tokens must be in [0, 2^21]");
   if (tokens == 0) return GPTQ_OK;
   if (!x) return fail(GPTQ_ERR_INVALID_ARG, w + " must not be NULL");
   if (!aligned_to(x, type_bytes(dtype)))

@@ -525,6 +525,8 @@ __global__ void __launch_bounds__(64 * kRowsWaves) w8a8_rows_kernel(GemmArgs a) 
 }
 
 constexpr int64_t kMaxRows = int64_t(1) << 24, kMaxTokens = int64_t(1) << 20;
+// A launch has at most 2^32 threads; a thread repacks 16 codes.
+constexpr int64_t kMaxCodes = int64_t(1) << 35;
 
 size_t codes_bytes(const gptq_w8a8_layer *l, int64_t tokens) {
   return align256(size_t(tokens) * l->k_pad);
@@ -673,7 +675,8 @@ extern "C" {
 
 size_t gptq_w8a8_layer_bytes(int64_t rows, int64_t cols) {
   if (rows < 1 || rows > kMaxRows || gptq_tokens_ld(cols) == 0) return 0;
-  return layer_map(nullptr, geometry(rows, cols)).bytes;
+  const Geometry g = geometry(rows, cols);
+  return g.rows_pad * g.k_pad > kMaxCodes ? 0 : layer_map(nullptr, g).bytes;
 }
 
 gptq_status gptq_w8a8_prepare(const uint8_t *q, const float *scale, const uint8_t *zero,

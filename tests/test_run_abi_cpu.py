@@ -33,7 +33,8 @@ def test_sizes():
     assert [L.gptq_tokens_ld(c) for c in (0, 1, 128, 129, 65536, 65537, -5)] == \
         [0, 128, 128, 256, 65536, 0, 0]
     assert L.gptq_w8a8_layer_bytes(17, 129) >= 32 * 256 + 2 * 32 * 4
-    for bad in ((0, 5), (5, 0), (5, 65537), ((1 << 24) + 1, 5)):
+    assert L.gptq_w8a8_layer_bytes(1 << 19, 65536) > 1 << 35
+    for bad in ((0, 5), (5, 0), (5, 65537), ((1 << 24) + 1, 5), ((1 << 19) + 1, 65536)):
         assert L.gptq_w8a8_layer_bytes(*bad) == 0
     assert L.gptq_w8a8_linear_ws_bytes(None, 4) == 0
     assert L.gptq_token_logprobs_ws_bytes(0, 100, 5) == 0
@@ -44,7 +45,8 @@ def test_sizes():
 
 @pytest.mark.parametrize("change,word", [
     (dict(x=None), "x must not be NULL"), (dict(x=A + 1), "aligned"), (dict(dtype=7), "type"),
-    (dict(tokens=-1), "tokens"), (dict(cols=0), "cols"), (dict(cols=70000), "cols"),
+    (dict(tokens=-1), "tokens"), (dict(tokens=(1 << 21) + 1), "tokens"),
+    (dict(cols=0), "cols"), (dict(cols=70000), "cols"),
     (dict(ld_x=299), "stride"), (dict(codes=None), "NULL"), (dict(codes=A + 8), "16-byte"),
     (dict(ld_codes=300), "ld_codes"), (dict(ld_codes=392), "ld_codes"), (dict(scale=None), "NULL"),
     (dict(sum=A + 2), "4-byte")])
@@ -131,8 +133,10 @@ def test_norm_block_refuses(change, word):
 @pytest.mark.parametrize("change,status,word", [
     (dict(logits=None), BAD, "logits"), (dict(logits=A + 1), BAD, "aligned"),
     (dict(ids=A + 4), BAD, "aligned"), (dict(dtype=8), BAD, "type"), (dict(rows=-1), BAD, "rows"),
+    (dict(rows=(1 << 23) + 1), BAD, "rows"),
     (dict(vocab=0), BAD, "vocab"), (dict(vocab=(1 << 24) + 1), BAD, "vocab"), (dict(ld=999), BAD, "ld"),
-    (dict(scale=0.0), BAD, "scale"), (dict(scale=1e31), BAD, "scale"), (dict(scale=float("inf")), BAD, "scale"),
+    (dict(scale=0.0), BAD, "scale"), (dict(scale=1e31), BAD, "scale"),
+    (dict(scale=float("inf")), BAD, "scale"),
     (dict(scale=float("nan")), BAD, "scale"), (dict(k=65), BAD, "top_k"),
     (dict(k=20, vocab=10, ld=10), BAD, "top_k"), (dict(top_ids=None), BAD, "top_ids"),
     (dict(ids=None), BAD, "ids"), (dict(entropy=A + 2), BAD, "aligned"),
