@@ -15,6 +15,7 @@
  *   gptq_silu_mul_quantize   as 8-bit codes with a scale per token
  *   gptq_w8a8_gemm,          the product on codes, or on float activations
  *   gptq_w8a8_linear         (quantized on the way)
+ *   gptq_gated_mlp_forward   a gated MLP block made of these, in one call
  *   gptq_token_logprobs      log probabilities of given tokens from logits,
  *                            whose mean is minus the log of the perplexity
  *                            the pages quote for quantized models ("GPTQ",
@@ -183,6 +184,41 @@ gptq_status gptq_norm_block(const gptq_norm_params *p, int32_t dtype,
                             void *h, int64_t ld_h, int8_t *codes,
                             int64_t ld_codes, float *scale, int32_t *sum,
                             void *stream);
+
+/* --------------------------------------------------------- gated MLP block
+ * With an input r of the residual stream (tokens x d):
+ *
+ *   x = codes(N_pre(r))             enter (its pre norm; r is scaled by its
+ *                                   residual_scale)
+ *   g, u = the halves of x W_gu^T   gate_up, 2 inner x d, rounded to dtype
+ *   b = codes(silu(g) u) W_d^T      down, d x inner, rounded to dtype
+ *   r', h                           leave, of r and b
+ *
+ * bit for bit what the calls above give one after the other.
+ */
+typedef struct {
+  gptq_norm_params enter, leave;
+  gptq_w8a8_layer gate_up, down;
+} gptq_gated_mlp;
+
+/* Scratch bytes (0 on invalid arguments). */
+size_t gptq_gated_mlp_ws_bytes(const gptq_gated_mlp *mlp, int32_t dtype,
+                               int64_t tokens);
+
+/*
+ *  dtype     type of r, gate, r_out, h and the stored intermediates.  tokens
+ *            <= 2^20, d <= 32768.
+ *  gate      of leave, as in gptq_norm_block.
+ *  r_out, h  as there; r_out may be r.  At least one is given.
+ *  ws        scratch, 256-byte aligned, >= gptq_gated_mlp_ws_bytes.
+ * On an error r_out and h are as before; ws may have been written.
+ */
+gptq_status gptq_gated_mlp_forward(const gptq_gated_mlp *mlp, int32_t dtype,
+                                   int64_t tokens, const void *r, int64_t ld_r,
+                                   const void *gate, int64_t ld_gate,
+                                   int64_t gate_tokens, void *r_out,
+                                   int64_t ld_r_out, void *h, int64_t ld_h,
+                                   void *ws, size_t ws_bytes, void *stream);
 
 /* ----------------------------------------------------------------- scoring
  * Per row of logits l (with z = scale l, p = softmax(z), in float32):

@@ -25,7 +25,8 @@ EXPORTED = (
     "gptq_tokens_ld", "gptq_quantize_tokens", "gptq_silu_mul_quantize",
     "gptq_w8a8_layer_bytes", "gptq_w8a8_prepare", "gptq_w8a8_gemm_ws_bytes",
     "gptq_w8a8_linear_ws_bytes", "gptq_w8a8_gemm", "gptq_w8a8_linear",
-    "gptq_norm_block", "gptq_token_logprobs_ws_bytes", "gptq_token_logprobs",
+    "gptq_norm_block", "gptq_gated_mlp_ws_bytes", "gptq_gated_mlp_forward",
+    "gptq_token_logprobs_ws_bytes", "gptq_token_logprobs",
 )
 
 
@@ -41,6 +42,11 @@ class gptq_norm_params(ctypes.Structure):
                 ("residual_scale", ctypes.c_float), ("block_scale", ctypes.c_float),
                 ("post_weight", ctypes.c_void_p), ("post_bias", ctypes.c_void_p),
                 ("pre_weight", ctypes.c_void_p), ("pre_bias", ctypes.c_void_p)]
+
+
+class gptq_gated_mlp(ctypes.Structure):
+    _fields_ = [("enter", gptq_norm_params), ("leave", gptq_norm_params),
+                ("gate_up", gptq_w8a8_layer), ("down", gptq_w8a8_layer)]
 
 
 _lib = None
@@ -66,6 +72,9 @@ def lib() -> ctypes.CDLL:
             ("gptq_w8a8_linear", I32, [layer, P, I32, I64, I64, P, I32, I64, P, SZ, P]),
             ("gptq_norm_block", I32, [ctypes.POINTER(gptq_norm_params), I32, I64, I64, P, I64, P,
                                       I64, P, I64, I64, P, I64, P, I64, P, I64, P, P, P]),
+            ("gptq_gated_mlp_ws_bytes", SZ, [ctypes.POINTER(gptq_gated_mlp), I32, I64]),
+            ("gptq_gated_mlp_forward", I32, [ctypes.POINTER(gptq_gated_mlp), I32, I64, P, I64, P,
+                                             I64, I64, P, I64, P, I64, P, SZ, P]),
             ("gptq_token_logprobs_ws_bytes", SZ, [I64, I64, I32]),
             ("gptq_token_logprobs", I32, [P, I32, I64, I64, I64, P, F, I32, P, P, P, P, P, P, SZ,
                                           P])):
@@ -99,7 +108,7 @@ def matrix(t: torch.Tensor, what: str, rows: int | None = None, cols: int | None
     """(address, row stride) of a device matrix whose rows are contiguous, of the
     given size and type where one is given."""
     shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1 and shape[0] > 0):
         raise ValueError(f"{what} must be a matrix with contiguous rows, got shape "
                          f"{tuple(shape)} and strides {stride}")
     r, c = shape
@@ -110,7 +119,7 @@ def matrix(t: torch.Tensor, what: str, rows: int | None = None, cols: int | None
         raise ValueError(f"{what} must be on the GPU")
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    return t.data_ptr(), stride[0] if r > 1 else c    # torch may report any for one row
+    return t.data_ptr(), stride[0] if r > 1 else c    # torch may report any for one row or none
 
 
 def ld(t: torch.Tensor) -> int:
@@ -245,6 +254,25 @@ def gptq_norm_block(params: gptq_norm_params, r, b=None, gate=None, gate_tokens:
         *(_NONE if h is None else matrix(h, "h", t, d, kind)),
         *(_NONE if codes is None else (codes.data_ptr(), ld(codes))),
         B._ptr(scale), B._ptr(sum), stream_ptr(r, stream)))
+
+
+def gptq_gated_mlp_ws_bytes(mlp: gptq_gated_mlp, dtype: torch.dtype, tokens: int) -> int:
+    return lib().gptq_gated_mlp_ws_bytes(mlp, DTYPES[dtype], tokens)
+
+
+def gptq_gated_mlp_forward(mlp: gptq_gated_mlp, r, gate=None, gate_tokens: int = 1, r_out=None,
+                           h=None, ws: int | None = None, ws_bytes: int = 0, stream=None):
+    """``ws``: address."""
+    kind = r.dtype
+    d = mlp.down.rows
+    ptr, stride = matrix(r, "r", None, d)
+    t = r.shape[0]
+    _check(lib().gptq_gated_mlp_forward(
+        mlp, _dtype(r, "r"), t, ptr, stride,
+        *(_NONE if gate is None else matrix(gate, "gate", None, d, kind)), gate_tokens,
+        *(_NONE if r_out is None else matrix(r_out, "r_out", t, d, kind)),
+        *(_NONE if h is None else matrix(h, "h", t, d, kind)),
+        ws, ws_bytes, stream_ptr(r, stream)))
 
 
 def gptq_token_logprobs_ws_bytes(rows: int, vocab: int, top_k: int) -> int:

@@ -1,22 +1,24 @@
 """A gated MLP block on per-row 8-bit layers: the blocks GatedMLPCalibrator
-quantizes, run on token codes.
+quantizes, run on token codes (gptq_gated_mlp_forward of gptq_run.h).
 
     codes(N_pre(r)) -> gate|up product -> codes(silu(g) u) -> down product b
     -> r' = alpha r + beta gate * N_post(b),  h = the next block's N_pre(r')
 
-Five launches; only g|u and b are stored in the stream's type."""
+Five launches from one call; only g|u and b are stored in the stream's type."""
 from __future__ import annotations
 
 import torch
 
-from .norms import NormBlock
-from .w8a8 import TokenCodes, W8A8Linear, silu_mul_quantize
+from . import binding_run as R
+from .norms import NormBlock, tokens_per_gate
+from .w8a8 import W8A8Linear
 
 
 class GatedMLP8:
     """``enter``: the NormBlock before the block; ``gate_up``: gate and up
     stacked along the rows; ``leave``: the NormBlock after it (its ``pre`` norm
-    is the next block's)."""
+    is the next block's).  Calls on different streams may overlap: each stream
+    has its own outputs and scratch memory."""
 
     def __init__(self, enter: NormBlock, gate_up: W8A8Linear, down: W8A8Linear,
                  leave: NormBlock):
@@ -24,33 +26,39 @@ class GatedMLP8:
             raise ValueError("gate_up must hold gate and up: twice down's input features")
         if not enter.d == gate_up.cols == down.rows == leave.d:
             raise ValueError("the norms, gate_up's inputs and down's outputs must agree in width")
-        self.enter, self.gate_up, self.down, self.leave = enter, gate_up, down, leave
+        self.enter, self.gate_up, self.down, self.leave = enter, gate_up, down, leave  # kept alive
         self.d, self.inner = down.rows, down.cols
-        self._buffers: dict = {}
+        self.block = R.gptq_gated_mlp(enter.params, leave.params, gate_up.layer, down.layer)
+        self.scratch = R.Scratch(down.device)
+        self._outputs: dict = {}
+        self._last = (-1, None, 0)      # tokens, type, scratch bytes
 
-    def buffers(self, tokens: int, dtype: torch.dtype, device, key: int):
-        """Activations of up to ``tokens`` tokens, one set per stream and type."""
-        kept = self._buffers.get((key, dtype))
-        if kept is None or kept[0].tokens < tokens:
-            def empty(cols):
-                return torch.empty((tokens, cols), dtype=dtype, device=device)
-            kept = (TokenCodes(tokens, self.d, device), empty(2 * self.inner),
-                    TokenCodes(tokens, self.inner, device), empty(self.d), empty(self.d),
-                    empty(self.d))
-            self._buffers[(key, dtype)] = kept
-        x, gu, a, b, r_out, h = kept
-        if x.tokens == tokens:
-            return kept
-        return (x.head(tokens), gu[:tokens], a.head(tokens), b[:tokens], r_out[:tokens],
-                h[:tokens])
+    def outputs(self, tokens: int, dtype: torch.dtype, stream) -> tuple:
+        """(r', h) of up to ``tokens`` tokens, one pair per stream and type."""
+        key = (R.stream_ptr(self.down.mem, stream), dtype)
+        kept = self._outputs.get(key)
+        if kept is None or kept[0].shape[0] < tokens:
+            with R.on(stream):
+                kept = tuple(torch.empty((tokens, self.d), dtype=dtype, device=self.down.device)
+                             for _ in range(2))
+            self._outputs[key] = kept
+        return kept if kept[0].shape[0] == tokens else tuple(t[:tokens] for t in kept)
 
-    def __call__(self, r: torch.Tensor, *, gate=None, gate_tokens: int | None = None):
-        """r: tokens x d, on the current stream.  Returns (r', h), which the next
-        call on this stream overwrites."""
-        key = torch.cuda.current_stream().cuda_stream
-        x, gu, a, b, r_out, h = self.buffers(r.shape[0], r.dtype, r.device, key)
-        self.enter(r, codes=x)
-        self.gate_up.product(x, gu)
-        silu_mul_quantize(gu[:, :self.inner], gu[:, self.inner:], a)
-        self.down.product(a, b)
-        return self.leave(r, b, gate=gate, gate_tokens=gate_tokens, r_out=r_out, h=h)
+    def __call__(self, r: torch.Tensor, *, gate=None, gate_tokens: int | None = None,
+                 stream=None):
+        """r: tokens x d; gate as for ``leave``.  Returns (r', h), which the next
+        call on the same stream overwrites."""
+        if r.dim() != 2 or r.shape[1] != self.d:
+            raise ValueError(f"r must be tokens x {self.d}, got {tuple(r.shape)}")
+        if not r.is_cuda:
+            raise ValueError("r must be on the GPU")
+        R._dtype(r, "r")
+        t = r.shape[0]
+        gate_tokens = 1 if gate is None else tokens_per_gate(gate, gate_tokens, t)
+        if self._last[:2] != (t, r.dtype):
+            self._last = (t, r.dtype, R.gptq_gated_mlp_ws_bytes(self.block, r.dtype, t))
+        n = self._last[2]
+        r_out, h = self.outputs(t, r.dtype, stream)
+        R.gptq_gated_mlp_forward(self.block, r, gate, gate_tokens, r_out, h,
+                                 self.scratch(n, r, stream), n, stream)
+        return r_out, h

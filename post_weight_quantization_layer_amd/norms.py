@@ -9,6 +9,17 @@ from . import binding_run as R
 from .w8a8 import TokenCodes
 
 
+def tokens_per_gate(gate: torch.Tensor, gate_tokens: int | None, tokens: int) -> int:
+    """Tokens that share a row of ``gate``: ``gate_tokens``, or by default all of
+    them for one row and one for several."""
+    if gate_tokens is None:
+        gate_tokens = max(tokens, 1) if gate.shape[0] == 1 else 1
+    if gate_tokens < 1 or gate.shape[0] * gate_tokens < tokens:
+        raise ValueError(f"{gate.shape[0]} gate rows of {gate_tokens} tokens do not "
+                         f"cover {tokens} tokens")
+    return gate_tokens
+
+
 class NormBlock:
     """r' = residual_scale r + block_scale gate * N_post(b);  h = N_pre(r').
 
@@ -43,14 +54,7 @@ class NormBlock:
         if r.dim() != 2 or r.shape[1] != self.d:
             raise ValueError(f"r must be tokens x {self.d}, got {tuple(r.shape)}")
         t = r.shape[0]
-        if gate is None:
-            gate_tokens = 1
-        else:
-            if gate_tokens is None:
-                gate_tokens = max(t, 1) if gate.shape[0] == 1 else 1
-            if gate_tokens < 1 or gate.shape[0] * gate_tokens < t:
-                raise ValueError(f"{gate.shape[0]} gate rows of {gate_tokens} tokens do not "
-                                 f"cover {t} tokens")
+        gate_tokens = 1 if gate is None else tokens_per_gate(gate, gate_tokens, t)
         if not r.is_cuda:
             raise ValueError("r must be on the GPU")
         if (r_out is None and b is not None) or (h is None and codes is None):

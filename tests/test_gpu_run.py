@@ -536,6 +536,34 @@ def test_gated_mlp_path():
         assert rel <= 4 * 2.0 ** -11
 
 
+@pytest.mark.parametrize("tokens,kind", [(1, "f16"), (7, "bf16"), (70, "f32"), (300, "f16"),
+                                         (0, "f16")])
+def test_gated_mlp_is_its_operators(tokens, kind):
+    """The one call gives the bits of the five, with a gate and rows apart."""
+    import torch
+    from post_weight_quantization_layer_amd.w8a8 import TokenCodes, silu_mul_quantize
+    rng = np.random.default_rng(23)
+    mlp, *_ = small_mlp(rng)
+    mlp.leave.params.residual_scale = 0.75
+    mlp.block.leave.residual_scale = 0.75
+    wide = to_gpu(activations(rng, tokens, 300), kind)
+    r = wide[:, 20:276]
+    gate = to_gpu(activations(rng, 3, 256), kind)
+    got = mlp(r, gate=gate, gate_tokens=100)
+    x = TokenCodes(tokens, 256)
+    mlp.enter(r, codes=x)
+    gu = mlp.gate_up.product(x, dtype=r.dtype)
+    a = silu_mul_quantize(gu[:, :384], gu[:, 384:])
+    b = mlp.down.product(a, dtype=r.dtype)
+    want = mlp.leave(r, b, gate=gate, gate_tokens=100)
+    for g, w in zip(got, want):
+        assert g.dtype == r.dtype and torch.equal(g, w)
+    with pytest.raises(ValueError):
+        mlp(r, gate=gate, gate_tokens=50 if tokens > 150 else 0)
+    with pytest.raises(TypeError):
+        mlp(r, gate=gate.double(), gate_tokens=100)
+
+
 def test_on_two_streams_and_in_a_graph():
     """The same bits on another stream and when replayed from a graph, with other
     work and synchronizations between the replays."""

@@ -153,6 +153,37 @@ def test_token_logprobs_refuses(change, status, word):
     assert st == status and said(word), B.gptq_last_error()
 
 
+def gated_mlp(enter=None, up=None, down=None):
+    norm = R.gptq_norm_params(0, 1, F16, 1e-6, 0.0, 1.0, 1.0, None, None, None, None)
+    return R.gptq_gated_mlp(enter or norm, norm, up or layer(600, 64), down or layer(64, 300))
+
+
+@pytest.mark.parametrize("change,status,word", [
+    (dict(mlp=None), BAD, "prepared"), (dict(mlp=gated_mlp(up=layer(600, 65))), BAD, "down.rows"),
+    (dict(mlp=gated_mlp(down=layer(64, 301))), BAD, "2 down.cols"),
+    (dict(mlp=gated_mlp(up=layer(600, 64, mem=None))), BAD, "prepared"),
+    (dict(dtype=4), BAD, "dtype"), (dict(tokens=-1), BAD, "tokens"),
+    (dict(tokens=(1 << 20) + 1), BAD, "tokens"), (dict(r_out=None, h=None), BAD, "one of"),
+    (dict(ws=None), WS, "NULL"), (dict(ws=A + 16), WS, "256-byte"), (dict(n=4096), WS, "too small"),
+    (dict(r=None), BAD, "r must"), (dict(ld_r=63), BAD, "stride"),
+    (dict(mlp=gated_mlp(enter=R.gptq_norm_params(0, 7, F16, 1e-6, 0.0, 1.0, 1.0, None, None, None,
+                                                 None))), BAD, "post and pre")])
+def test_gated_mlp_refuses(change, status, word):
+    a = dict(mlp=gated_mlp(), dtype=F16, tokens=4, r=A, ld_r=64, r_out=A, h=A, ws=A, n=1 << 30)
+    a.update(change)
+    st = R.lib().gptq_gated_mlp_forward(a["mlp"], a["dtype"], a["tokens"], a["r"], a["ld_r"], None,
+                                        0, 1, a["r_out"], 64, a["h"], 64, a["ws"], a["n"], None)
+    assert st == status and said(word), B.gptq_last_error()
+
+
+def test_gated_mlp_scratch():
+    f = R.lib().gptq_gated_mlp_ws_bytes
+    # codes of 4 rows of 128 and 384, 4 x 600 and 4 x 64 values
+    assert f(gated_mlp(), F16, 4) >= 4 * (128 + 384) + 2 * 4 * 664
+    assert f(gated_mlp(), F32, 4) > f(gated_mlp(), F16, 4)
+    assert f(None, F16, 4) == f(gated_mlp(), 9, 4) == f(gated_mlp(), F16, 0) == 0
+
+
 def test_zero_tokens_are_no_ops():
     L = R.lib()
     p = R.gptq_norm_params(1, 1, F16, 1e-6, 0.0, 1.0, 1.0, None, None, None, None)
@@ -162,6 +193,8 @@ def test_zero_tokens_are_no_ops():
     assert L.gptq_w8a8_gemm(layer(), None, 0, None, None, 0, None, F16, 64, None, 0, None) == OK
     assert L.gptq_norm_block(p, F16, 0, 64, None, 64, None, 0, None, 0, 1, None, 64, None, 0, None,
                              0, None, None, None) == OK
+    assert L.gptq_gated_mlp_forward(gated_mlp(), F16, 0, None, 64, None, 0, 1, None, 64, None, 64,
+                                    None, 0, None) == OK
     assert L.gptq_token_logprobs(None, F32, 0, 100, 100, None, 1.0, 0, None, None, None, None,
                                  None, None, 0, None) == OK
 
