@@ -107,6 +107,11 @@ def matrix(t: torch.Tensor, what: str, rows: int | None = None, cols: int | None
            dtype: torch.dtype | None = None) -> tuple[int, int]:
     """(address, row stride) of a device matrix whose rows are contiguous, of the
     given size and type where one is given."""
+    if t.is_contiguous() and t.dim() == 2:
+        r, c = t.shape
+        if (rows is None or r == rows) and (cols is None or c == cols) and t.is_cuda and \
+                (dtype is None or t.dtype is dtype):
+            return t.data_ptr(), c
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1 and shape[0] > 0):
         raise ValueError(f"{what} must be a matrix with contiguous rows, got shape "
@@ -242,18 +247,30 @@ def gptq_w8a8_linear(layer: gptq_w8a8_layer, x, y, ws: int | None = None, ws_byt
 _NONE = (None, 0)
 
 
+def like(t: torch.Tensor | None, what: str, shape: torch.Size, dtype: torch.dtype):
+    """matrix() of a tensor that has to be like another; of None: (None, 0)."""
+    if t is None:
+        return _NONE
+    if t.shape == shape and t.is_contiguous() and t.dtype is dtype and t.is_cuda:
+        return t.data_ptr(), shape[1]
+    return matrix(t, what, *shape, dtype)
+
+
 def gptq_norm_block(params: gptq_norm_params, r, b=None, gate=None, gate_tokens: int = 1,
                     r_out=None, h=None, codes=None, scale=None, sum=None, stream=None):
-    t, d = r.shape
-    kind = r.dtype
-    _check(lib().gptq_norm_block(
-        params, _dtype(r, "r"), t, d, *matrix(r, "r"),
-        *(_NONE if b is None else matrix(b, "b", t, d, kind)),
-        *(_NONE if gate is None else matrix(gate, "gate", None, d, kind)), gate_tokens,
-        *(_NONE if r_out is None else matrix(r_out, "r_out", t, d, kind)),
-        *(_NONE if h is None else matrix(h, "h", t, d, kind)),
-        *(_NONE if codes is None else (codes.data_ptr(), ld(codes))),
-        B._ptr(scale), B._ptr(sum), stream_ptr(r, stream)))
+    ptr, stride = matrix(r, "r")
+    shape, kind = r.shape, r.dtype
+    gptr, gstride = _NONE if gate is None else matrix(gate, "gate", None, shape[1], kind)
+    bptr, bstride = like(b, "b", shape, kind)
+    optr, ostride = like(r_out, "r_out", shape, kind)
+    hptr, hstride = like(h, "h", shape, kind)
+    c = s = n = None
+    ldc = 0
+    if codes is not None:
+        c, ldc, s, n = codes.data_ptr(), ld(codes), scale.data_ptr(), sum.data_ptr()
+    _check((_lib or lib()).gptq_norm_block(
+        params, _dtype(r, "r"), *shape, ptr, stride, bptr, bstride, gptr, gstride, gate_tokens,
+        optr, ostride, hptr, hstride, c, ldc, s, n, stream_ptr(r, stream)))
 
 
 def gptq_gated_mlp_ws_bytes(mlp: gptq_gated_mlp, dtype: torch.dtype, tokens: int) -> int:
@@ -266,12 +283,11 @@ def gptq_gated_mlp_forward(mlp: gptq_gated_mlp, r, gate=None, gate_tokens: int =
     kind = r.dtype
     d = mlp.down.rows
     ptr, stride = matrix(r, "r", None, d)
-    t = r.shape[0]
+    shape = r.shape
     _check(lib().gptq_gated_mlp_forward(
-        mlp, _dtype(r, "r"), t, ptr, stride,
+        mlp, _dtype(r, "r"), shape[0], ptr, stride,
         *(_NONE if gate is None else matrix(gate, "gate", None, d, kind)), gate_tokens,
-        *(_NONE if r_out is None else matrix(r_out, "r_out", t, d, kind)),
-        *(_NONE if h is None else matrix(h, "h", t, d, kind)),
+        *like(r_out, "r_out", shape, kind), *like(h, "h", shape, kind),
         ws, ws_bytes, stream_ptr(r, stream)))
 
 

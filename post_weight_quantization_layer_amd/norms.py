@@ -51,13 +51,14 @@ class NormBlock:
         None and b is given, not written if None and b is None).  h goes to
         ``h`` and / or, as codes, to ``codes``; the second result is ``codes``
         where only that is given, and a new tensor where neither is."""
-        if r.dim() != 2 or r.shape[1] != self.d:
-            raise ValueError(f"r must be tokens x {self.d}, got {tuple(r.shape)}")
-        t = r.shape[0]
+        shape = r.shape
+        if len(shape) != 2 or shape[1] != self.d:
+            raise ValueError(f"r must be tokens x {self.d}, got {tuple(shape)}")
+        t = shape[0]
         gate_tokens = 1 if gate is None else tokens_per_gate(gate, gate_tokens, t)
-        if not r.is_cuda:
-            raise ValueError("r must be on the GPU")
         if (r_out is None and b is not None) or (h is None and codes is None):
+            if not r.is_cuda:
+                raise ValueError("r must be on the GPU")
             with R.on(stream):
                 if r_out is None and b is not None:
                     r_out = torch.empty((t, self.d), dtype=r.dtype, device=r.device)
