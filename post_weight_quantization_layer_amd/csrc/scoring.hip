@@ -18,8 +18,8 @@
 // selections go by (value, lower index), so the result does not depend on the
 // order of the work.
 //
-// 4096 x 128000 bf16: 189 us without alternatives, 5.5 TB/s, bound by memory;
-// 219 us with 20, 266 us with 64.  1 x 32000: 6.7 us and 2.8 us for the join, a
+// 4096 x 128000 bf16: 190 us without alternatives, 5.5 TB/s, bound by memory;
+// 222 us with 20, 266 us with 64.  1 x 32000: 6.7 us and 2.8 us for the join, a
 // chain of dependent steps.
 #include <algorithm>
 
@@ -47,7 +47,7 @@ struct ScoreArgs {
   const void *logits;
   const int64_t *ids;
   int64_t ld;
-  int vocab, k, splits, seg;    // seg: elements per split (a multiple of kTile)
+  int vocab, k, splits, seg;    // seg: elements per split (a multiple of 16)
   float scale;
   float *logprob;
   int *rank;
@@ -124,63 +124,71 @@ __device__ __forceinline__ uint32_t common_prefix(uint32_t all, int first) {
   return first < 0 ? all : all & ~((2u << first) - 1);
 }
 
-// Cuts the list of n keys to its k best, exactly (k < n <= kListCap), and
-// returns the smallest kept value.  The k-th largest value is searched bit by
-// bit, counting with ballots, from the first bit that differs within the list;
-// if more than k entries reach it, their lowest indices are searched the same
-// way.  One wave; the list is in its LDS.
-__device__ __forceinline__ float cut_list(uint64_t *list, int n, int k) {
-  constexpr int kPer = (kListCap + 63) / 64;   // 11
-  const int lane = threadIdx.x & 63;
-  uint32_t hi[kPer], lo[kPer];
-  uint32_t any = 0, all = ~0u;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const uint64_t e = lane + 64 * i < n ? list[lane + 64 * i] : 0;
-    hi[i] = uint32_t(e >> 32);
-    lo[i] = uint32_t(e);
-    if (lane + 64 * i < n) any |= hi[i], all &= hi[i];
-  }
-  const int used = (n + 63) / 64;
-  any = wave_all<OrU>(any);
-  all = wave_all<AndU>(all);
+// The largest value that k of a wave's entries v (kListLane to a lane) reach, or,
+// where several entries are equal, the value from which more than k do; `reach`
+// is the number that reach it (at first: all entries that count).  Searched bit
+// by bit, counting with ballots, over the bits in which the entries differ
+// (`any`, `all`: their or and and); entries that do not count are 0.
+constexpr int kListLane = (kListCap + 63) / 64;   // 11
+__device__ __forceinline__ uint32_t kth_of(const uint32_t (&v)[kListLane], int k, uint32_t any,
+                                           uint32_t all, int &reach) {
   const int first = first_differing(any, all);
   uint32_t value = common_prefix(all, first);
-  int reach = n;                        // entries >= value
   for (int bit = first; bit >= 0 && reach > k; --bit) {
     const uint32_t probe = value | (1u << bit);
+    if (!((any ^ all) >> bit & 1)) {
+      value |= all & (1u << bit);
+      continue;
+    }
     int c = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (i >= used) break;
-      c += __popcll(__ballot(hi[i] >= probe));
-    }
+    for (int i = 0; i < kListLane; ++i) c += __popcll(__ballot(v[i] >= probe));
     if (c >= k) value = probe, reach = c;
   }
-  uint32_t low = 0;                     // of those equal to value: keep lo >= low
-  if (reach > k) {
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t probe = low | (1u << bit);
-      int c = 0;
+  return value;
+}
+
+// Cuts the list of n keys to its k best, exactly (k < n <= kListCap), and
+// returns the smallest kept value: the k-th largest value and, if more than k
+// entries reach it, the lowest of the indices to keep among equals.  One wave;
+// the list is in its LDS, read again at each step so that only one word per
+// entry stays in registers (80 per lane in all, six workgroups per compute unit;
+// with 95 and five, 6276 x 16586 with 64 alternatives took 105 us against 93).
+// No branch per 64 entries in the search, and none of the bits that all entries
+// share: 300 x 500 with 64 alternatives 19 us, 36 with both.
+__device__ __forceinline__ float cut_list(uint64_t *list, int n, int k) {
+  const int lane = threadIdx.x & 63;
+  uint32_t v[kListLane];                 // an entry's value; then its index
+  uint32_t any = 0, all = ~0u;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (i >= used) break;
-        c += __popcll(__ballot(hi[i] > value || (hi[i] == value && lo[i] >= probe)));
-      }
-      if (c >= k) low = probe;
-      if (c == k) break;
-    }
+  for (int i = 0; i < kListLane; ++i) {
+    const bool entry = lane + 64 * i < n;
+    v[i] = entry ? uint32_t(list[lane + 64 * i] >> 32) : 0;   // above 0 in every entry
+    any |= v[i];
+    if (entry) all &= v[i];
   }
+  int reach = n;
+  const uint32_t value = kth_of(v, k, wave_all<OrU>(any), wave_all<AndU>(all), reach);
+  // Entries above the value count always, those equal to it by index.
+  any = 0, all = ~0u;
+#pragma unroll
+  for (int i = 0; i < kListLane; ++i) {
+    const uint32_t at = v[i];
+    v[i] = at > value ? ~0u : at == value ? uint32_t(list[lane + 64 * i]) : 0u;
+    if (at == value) any |= v[i], all &= v[i];
+  }
+  uint32_t from = 1;
+  if (reach > k) from = kth_of(v, k, wave_all<OrU>(any), wave_all<AndU>(all), reach);
   int at = 0;
   uint32_t least = ~0u;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    if (i >= used) break;
-    const bool keep = hi[i] > value || (hi[i] == value && lo[i] >= low && lane + 64 * i < n);
+  for (int i = 0; i < kListLane; ++i) {
+    const bool keep = v[i] >= from;
     const uint64_t mask = __ballot(keep);
-    if (keep) {
-      list[at + __popcll(mask & ((uint64_t(1) << lane) - 1))] = (uint64_t(hi[i]) << 32) | lo[i];
-      least = min(least, hi[i]);
+    if (keep) {                          // to a place below the entries not read yet
+      const uint64_t e = list[lane + 64 * i];
+      list[at + __popcll(mask & ((uint64_t(1) << lane) - 1))] = e;
+      least = min(least, uint32_t(e >> 32));
     }
     at += __popcll(mask);
   }
@@ -608,9 +616,12 @@ __global__ void __launch_bounds__(kThreads) score_join_kernel(ScoreArgs a) {
   if (tid >= total && tid < a.k) write_top(a, row, tid, o, false, 0);
 }
 
-// A row is split over workgroups, by whole tiles, until there is about one of
-// them per compute unit (16 x 128000 with 20 alternatives: 13.4 us, 17.1 with
-// four per unit, whose join has more to rank).
+// A row is split over workgroups until there is about one of them per compute
+// unit (16 x 128000 with 20 alternatives: 13.4 us, 17.1 with four per unit, whose
+// join has more to rank).  The parts have no more tiles than whole ones would
+// and about equal lengths: one of fewer than 8 k elements has no threshold and
+// lists all it has (96 x 24799 with 64 alternatives in parts of 12288, 12288 and
+// 223: 28 us, 16 in equal ones).
 struct ScorePlan {
   int splits, seg;
 };
@@ -618,8 +629,8 @@ ScorePlan score_plan(int64_t rows, int64_t vocab, int32_t k, int cus) {
   const int64_t tiles = cdiv(vocab, kTile);
   const int64_t most = std::min<int64_t>(kMaxSplits, kMaxJoin / std::max(k, 1));
   const int64_t want = std::min<int64_t>({tiles, cdiv(cus, rows), most});
-  const int64_t per = cdiv(tiles, want);
-  return {int(cdiv(tiles, per)), int(per * kTile)};
+  const int64_t splits = cdiv(tiles, cdiv(tiles, want));
+  return {int(splits), int(cdiv(cdiv(vocab, splits), 16) * 16)};
 }
 
 constexpr size_t kPartBytes = kPartWords * sizeof(float);
