@@ -635,9 +635,10 @@ gptq_status launch_tiles(const GemmArgs &a, int splits, hipStream_t s) {
   const int rt = int(cdiv(a.rows, 32 * FA)), tt = int(cdiv(a.tokens, 32 * FB));
   const uint32_t tiles = uint32_t(rt) * uint32_t(tt);
   GPTQ_TRY(launch("w8a8_gemm", kern, dim3(tiles * splits), dim3(256), lds, s, a, tt, rt, splits));
-  if (!SPLIT) return GPTQ_OK;
-  return launch("w8a8_join", w8a8_join_kernel<FA, FB>, dim3(tiles * FA), dim3(256), 0, s, a, tt,
-                rt, splits);
+  if constexpr (SPLIT)
+    GPTQ_TRY(launch("w8a8_join", w8a8_join_kernel<FA, FB>, dim3(tiles * FA), dim3(256), 0, s, a, tt,
+                    rt, splits));
+  return GPTQ_OK;
 }
 
 gptq_status gemm_launch(const gptq_w8a8_layer *l, const int8_t *codes, int64_t ld_codes,
