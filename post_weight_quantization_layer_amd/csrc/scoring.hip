@@ -99,10 +99,16 @@ __device__ __forceinline__ float exponent(float l, float m, float c) {
 struct Stat {
   float m, s, t;
 };
+// What takes sums at the maximum `from` to the maximum m: the difference of their
+// references, not exponent()'s, which would keep a part of the rounding of c m
+// each time (and is 0 where they are equal).
+__device__ __forceinline__ float shift(float from, float m, float c) {
+  const float M = reference(m, c);
+  return fabsf(M) < kLarge ? reference(from, c) - M : exponent(from, m, c);
+}
 // The part at its own maximum, rescaled to the maximum m.
 __device__ __forceinline__ Stat rescaled(const Stat &a, float m, float c) {
-  const float M = reference(m, c);
-  const float d = fabsf(M) < kLarge ? reference(a.m, c) - M : exponent(a.m, m, c);
+  const float d = shift(a.m, m, c);
   const float f = exp2f(d);
   // a part scaled to nothing adds nothing (its t would be 0 * infinity); a NaN
   // in s stays
@@ -411,7 +417,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
       }
     } else {
       // Some lane has only -infinity or huge values so far.
-      const float dm = exponent(st.m, m, c), f = exp2f(dm);
+      const float dm = shift(st.m, m, c), f = exp2f(dm);
       st.t = f > 0.f ? f * (st.t + dm * st.s) : 0.f;
       st.s *= f;
 #pragma unroll

@@ -481,6 +481,19 @@ def test_scores_masks_and_special_values():
     check_scores(y, ids, "f16", 1.0, 64, "odd", "special f16")
 
 
+@pytest.mark.parametrize("rows,vocab", [(300, 30011), (2, 130000), (600, 9000)])
+def test_scores_of_few_allowed_tokens_far_from_zero(rows, vocab):
+    """Large logits at a few places, so that most of a row never holds a finite
+    value: the sums are taken from tile to tile without drifting."""
+    rng = np.random.default_rng(vocab)
+    x = np.full((rows, vocab), -np.inf, dtype=np.float32)
+    at = rng.integers(0, 4000, (rows, 3))
+    np.put_along_axis(x, at, (97.3 + rng.standard_normal((rows, 3))).astype(np.float32), axis=1)
+    x[1::2, vocab - 7] = 96.1
+    for scale in (1.0, 2.5):
+        check_scores(x, at[:, 0], "f32", scale, 2, "plain", f"few {rows}x{vocab}")
+
+
 def test_scores_of_empty_wide_and_without_ids():
     import torch
     from post_weight_quantization_layer_amd.scoring import TokenScorer
