@@ -509,6 +509,64 @@ def test_scores_of_empty_wide_and_without_ids():
     assert sc(x[:0], torch.zeros(0, dtype=torch.int64, device="cuda")).logprob.numel() == 0
 
 
+# ------------------------------------------------------------ far offsets
+
+def test_offsets_past_32_bits():
+    """Rows whose elements lie more than 2^32 apart, of inputs and of outputs,
+    give what the same rows close together give."""
+    import torch
+    from post_weight_quantization_layer_amd.norms import NormBlock
+    from post_weight_quantization_layer_amd.scoring import TokenScorer
+    from post_weight_quantization_layer_amd.w8a8 import quantize_tokens
+    rng = np.random.default_rng(31)
+    stride, cols = (1 << 31) + 24, 1000
+
+    def far():
+        store = torch.empty(2 * stride + cols, dtype=torch.float16, device="cuda")
+        return store.as_strided((3, cols), (stride, 1))
+
+    x, y = far(), far()
+    near = to_gpu(rng.standard_normal((3, cols)), "f16")
+    x.copy_(near)
+    ids = torch.arange(3, device="cuda")
+    for a, b in zip(vars(TokenScorer(3, cols, 5)(x, ids)).values(),
+                    vars(TokenScorer(3, cols, 5)(near, ids)).values()):
+        assert torch.equal(a, b)
+    qa, qb = quantize_tokens(x), quantize_tokens(near)
+    assert torch.equal(qa.codes, qb.codes) and torch.equal(qa.scale, qb.scale)
+    layer = layer_on_gpu(*stored_layer(rng, cols, cols))
+    assert torch.equal(layer(x, y), layer(near))
+    # 40 tokens: tiles, with token rows of codes that far apart in y
+    wide = torch.empty(39 * (1 << 27) + cols, dtype=torch.float16, device="cuda")
+    wide = wide.as_strided((40, cols), (1 << 27, 1))
+    many = to_gpu(rng.standard_normal((40, cols)), "f16")
+    assert torch.equal(layer(many, wide), layer(many))
+    norm = NormBlock(cols, post="rms", pre="layer")
+    want = norm(near, near)
+    got = norm(x, x, r_out=y, h=x)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_a_layer_of_more_than_2_32_codes():
+    """The last rows of a layer whose codes pass 2^32 bytes, for a token and for
+    40, against the same rows as a layer of their own."""
+    import torch
+    from post_weight_quantization_layer_amd.w8a8 import W8A8Linear
+    rows, cols, last = (1 << 17) + 300, 32768 + 128, 500
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(32)
+    q = torch.randint(0, 256, (rows, cols), device="cuda", dtype=torch.uint8, generator=gen)
+    scale = torch.rand(rows, device="cuda", generator=gen)
+    zero = torch.randint(0, 256, (rows,), device="cuda", dtype=torch.uint8, generator=gen)
+    whole = W8A8Linear(q, scale, zero)
+    part = W8A8Linear(q[-last:].contiguous(), scale[-last:].contiguous(), zero[-last:].contiguous())
+    for tokens in (1, 40):
+        x = torch.randn((tokens, cols), device="cuda", generator=gen).half()
+        y = torch.empty((tokens, rows), dtype=torch.float32, device="cuda")
+        z = torch.empty((tokens, last), dtype=torch.float32, device="cuda")
+        assert torch.equal(whole(x, y)[:, -last:], part(x, z))
+
+
 # ----------------------------------------------------- streams, graphs, path
 
 def small_mlp(rng, d=256, inner=384):
