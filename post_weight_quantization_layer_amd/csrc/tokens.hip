@@ -336,6 +336,8 @@ RowShape row_shape(int64_t n, int64_t rows, int cus) {
   if (lanes <= 256) return {4, 1};
   if (lanes <= 512) return many ? RowShape{4, 2} : RowShape{8, 1};
   if (lanes <= 1024) return {8, 2};
+  if (many && lanes <= 1536) return {8, 3};
+  if (many && lanes <= 2048) return {8, 4};
   return {16, lanes <= 2048 ? 2 : 4};
 }
 
@@ -348,6 +350,8 @@ gptq_status with_shape(RowShape s, F &&f) {
     case 4 * 8 + 2: return f.template operator()<E, 4, 2>();
     case 8 * 8 + 1: return f.template operator()<E, 8, 1>();
     case 8 * 8 + 2: return f.template operator()<E, 8, 2>();
+    case 8 * 8 + 3: return f.template operator()<E, 8, 3>();
+    case 8 * 8 + 4: return f.template operator()<E, 8, 4>();
     case 16 * 8 + 2: return f.template operator()<E, 16, 2>();
     default: return f.template operator()<E, 16, 4>();
   }
