@@ -322,6 +322,15 @@ def test_norm_block(kind, t, d, post, pre, gates, w_kind, how):
         block_scale=1.5, eps=eps, weight_offset=off)[1], rtol=1e-9, atol=1e-12)
 
 
+@pytest.mark.parametrize("kind,t,d,how", [
+    ("bf16", 4097, 2040, "plain"), ("f32", 4096, 1537, "odd"), ("f16", 1024, 16001, "odd"),
+    ("bf16", 1025, 4096, "plain"), ("f32", 1024, 8191, "left"), ("f16", 1030, 1290, "left")])
+def test_norm_block_and_codes_of_many_rows(kind, t, d, how):
+    """Every division of a row over waves that many rows take."""
+    test_norm_block(kind, t, d, "layer", "rms", "pairs", "same", how)
+    test_quantize_tokens(kind, t, d, how)
+
+
 @pytest.mark.parametrize("t,d", [(1, 4096), (3, 130), (1024, 1000), (6, 8200)])
 def test_norm_block_in_place_codes_and_first(t, d):
     """In place equals out of place; codes are those of the float32 h; no block output."""
