@@ -24,10 +24,10 @@ struct BlockWs {
 };
 
 BlockWs block_ws(const gptq_gated_mlp *m, int32_t dtype, int64_t tokens, void *mem) {
-  char *const base = static_cast<char *>(mem);
+  const uintptr_t base = reinterpret_cast<uintptr_t>(mem);   // 0 where only the size is asked
   size_t at = 0;
   auto take = [&](size_t n) {
-    char *p = base + at;
+    char *p = reinterpret_cast<char *>(base + at);
     at += align256(n);
     return p;
   };

@@ -46,7 +46,7 @@ struct LayerMap {
   size_t bytes;
 };
 LayerMap layer_map(void *mem, const Geometry &g) {
-  char *p = static_cast<char *>(mem);
+  const uintptr_t p = reinterpret_cast<uintptr_t>(mem);    // 0 where only the size is asked
   const size_t codes = align256(size_t(g.rows_pad) * g.k_pad);
   const size_t vec = align256(size_t(g.rows_pad) * 4);
   return {reinterpret_cast<int8_t *>(p), reinterpret_cast<float *>(p + codes),
