@@ -3,7 +3,7 @@
 //
 // With c = scale log2 e, every lane keeps a running maximum m of its logits,
 // s = sum 2^(c l - M) and t = sum (c l - M) 2^(c l - M), M being the float
-// nearest c m; lanes, waves and, when a row is split over workgroups, parts
+// nearest c m (c m itself from 2^22 up); lanes, waves and, when a row is split over workgroups, parts
 // are joined by rescaling to the common maximum.  Then ln p = ln 2 (c l - M) -
 // ln s and the entropy is ln s - ln 2 t / s.  c l - M is one fused operation,
 // exact up to its last rounding because M, not c m, is the reference.
@@ -81,9 +81,12 @@ __device__ __forceinline__ uint64_t make_key(float v, int index) {
 __device__ __forceinline__ float key_value(uint64_t key) { return from_ordered(uint32_t(key >> 32)); }
 __device__ __forceinline__ int key_index(uint64_t key) { return int(~uint32_t(key)); }
 
-// c l - M for a row maximum m.  Where c m is too large for that (a row of
-// masks at the type's lowest value), c (l - m), halved against overflow.
-constexpr float kLarge = 1e30f;
+// c l - M for a row maximum m.  M is off c m by up to half a unit in its last
+// place, which every difference to it carries and the sums' scale with them: 1/4
+// below kLarge, harmless, but beyond 2^7 powers of two of such differences leave
+// float32 (a lane that has seen nothing but masks of -1e10).  From kLarge up the
+// sums are relative to c m itself: c (l - m), halved against overflow.
+constexpr float kLarge = 4194304.f;
 // M: the product rounded, never fused into what uses it.
 __device__ __forceinline__ float reference(float m, float c) {
   float M = m * c;
@@ -100,11 +103,12 @@ struct Stat {
   float m, s, t;
 };
 // What takes sums at the maximum `from` to the maximum m: the difference of their
-// references, not exponent()'s, which would keep a part of the rounding of c m
-// each time (and is 0 where they are equal).
+// references, each M or c m by its own size.  (With exponent()'s the sums would keep a
+// part of the rounding of c m each time; this is 0 where they are equal.)
 __device__ __forceinline__ float shift(float from, float m, float c) {
-  const float M = reference(m, c);
-  return fabsf(M) < kLarge ? reference(from, c) - M : exponent(from, m, c);
+  const float F = reference(from, c), M = reference(m, c);
+  if (fabsf(M) < kLarge) return fabsf(F) < kLarge ? F - M : __builtin_fmaf(from, c, -M);
+  return fabsf(F) < kLarge ? -__builtin_fmaf(m, c, -F) : exponent(from, m, c);
 }
 // The part at its own maximum, rescaled to the maximum m.
 __device__ __forceinline__ Stat rescaled(const Stat &a, float m, float c) {
@@ -249,8 +253,10 @@ struct RowOut {
 };
 // ln p of an entry of value l (not of an empty row).
 __device__ __forceinline__ float log_prob(const ScoreArgs &a, const RowOut &o, float l) {
-  const bool plain = fabsf(o.m * o.c) < kLarge && fabsf(l * o.c) < kLarge;
-  const float d = plain ? kLn2 * exponent(l, o.m, o.c) : (0.5f * l - 0.5f * o.m) * a.scale * 2.f;
+  const float M = reference(o.m, o.c), z = __builtin_fmaf(l, o.c, -M);
+  // c l may overflow where scale (l - m) does not
+  const bool plain = fabsf(M) < kLarge && z > -3e38f;
+  const float d = plain ? kLn2 * z : (0.5f * l - 0.5f * o.m) * a.scale * 2.f;
   return d - o.log_s;
 }
 __device__ __forceinline__ RowOut finish_row(const ScoreArgs &a, const Stat &st, int rank_count,
@@ -375,10 +381,10 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
     float m = st.m;
 #pragma unroll
     for (int q = 0; q < kUnroll; ++q) m = fmaxf(m, cmax[q]);
-    const float M = reference(m, c);
-    if (!__ballot(!(fabsf(M) < kLarge))) {
-      // (a lane whose elements were all -infinity so far has s = t = 0)
-      const float dm = fmaxf(reference(st.m, c) - M, -200.f), f = __builtin_amdgcn_exp2f(dm);
+    const float M = reference(m, c), from = reference(st.m, c);
+    // (a lane whose elements were all -infinity so far has s = t = 0)
+    if (!__ballot(!(fabsf(M) < kLarge) || (!(fabsf(from) < kLarge) && st.s != 0.f))) {
+      const float dm = fmaxf(from - M, -200.f), f = __builtin_amdgcn_exp2f(dm);
       st.t = f * (st.t + dm * st.s);
       st.s *= f;
       if (!masked) {
@@ -416,7 +422,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
           }
       }
     } else {
-      // Some lane has only -infinity or huge values so far.
+      // Some lane has only -infinity or huge values so far, or had until now.
       const float dm = shift(st.m, m, c), f = exp2f(dm);
       st.t = f > 0.f ? f * (st.t + dm * st.s) : 0.f;
       st.s *= f;
