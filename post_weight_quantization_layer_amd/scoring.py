@@ -17,15 +17,24 @@ class TokenLogprobs:
     entropy: torch.Tensor               # rows float32
     top_ids: torch.Tensor               # rows x top_k int32, -1 past the last alternative
     top_logprobs: torch.Tensor          # rows x top_k float32
+    ids: torch.Tensor | None = None     # the given tokens: the caller's tensor itself
 
     def perplexity(self) -> float:
         """exp of minus the mean log probability over the rows that have a given
-        token (synchronizes)."""
-        scored = self.rank >= 0
-        n = int(scored.sum())
+        token (id >= 0; synchronizes).  NaN where such a row could not be scored
+        (it holds a NaN or +infinity, or its id is past the vocabulary) and where
+        no row has a token; infinity where a token is impossible or the mean is
+        past exp's range.  Reads ``ids``, which must not have changed."""
+        if self.ids is None:
+            raise ValueError("no perplexity without ids: the call was given no tokens")
+        given = self.ids.view(-1) >= 0
+        n = int(given.sum())
         if n == 0:
             return math.nan
-        return math.exp(-float(self.logprob[scored].double().sum()) / n)
+        try:
+            return math.exp(-float(self.logprob[given].double().sum()) / n)
+        except OverflowError:
+            return math.inf
 
 
 class TokenScorer:
@@ -66,6 +75,7 @@ class TokenScorer:
             out = TokenLogprobs(None, None, out.entropy, out.top_ids, out.top_logprobs)
         else:
             R.vector(ids, "ids", n, torch.int64)
+            out.ids = ids
         if self._last[0] != n:
             self._last = (n, R.gptq_token_logprobs_ws_bytes(n, self.vocab, self.top_k))
         nbytes = self._last[1]
