@@ -140,37 +140,57 @@ def vector(t: torch.Tensor, what: str, n: int, dtype: torch.dtype | None = None)
     return t
 
 
-@contextlib.contextmanager
+_CURRENT = contextlib.nullcontext()
+
+
 def on(stream):
     """Allocations inside belong to ``stream`` (None: the current one)."""
     if stream is None:
-        yield
-        return
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
-    with torch.cuda.stream(s):
-        yield
+        return _CURRENT
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream)
+                             else torch.cuda.ExternalStream(stream))
+
+
+def capturing(stream=None) -> bool:
+    """Whether ``stream`` (None: the current one) is being captured into a graph."""
+    if stream is None:
+        return torch._C._cuda_isCurrentStreamCapturing()
+    with on(stream):
+        return torch._C._cuda_isCurrentStreamCapturing()
 
 
 class Scratch:
     """Workspace of an object, one per stream that uses it, so that calls on
-    several streams do not share one; grows to the largest request."""
+    several streams do not share one; grows to the largest request.
+
+    A call that is being captured gets a buffer of its own, from the graph's
+    pool: the graph may be replayed after a larger call has replaced the stream's
+    buffer, or beside a call that uses it."""
 
     def __init__(self, device):
         self.device = device
         self._by_stream: dict[int, torch.Tensor] = {}
 
-    def __call__(self, nbytes: int, like: torch.Tensor, stream=None) -> int | None:
-        """Address of at least ``nbytes`` bytes for use on ``stream`` (None: the
-        current stream of ``like``'s device)."""
+    def __call__(self, nbytes: int, like: torch.Tensor, stream=None) -> torch.Tensor | None:
+        """At least ``nbytes`` bytes for one call on ``stream`` (None: the current
+        stream of ``like``'s device), to be held until its launches are issued."""
         if nbytes == 0:
             return None
+        if capturing(stream):
+            return self._new(nbytes, stream)
         ptr = stream_ptr(like, stream)
         t = self._by_stream.get(ptr)
         if t is None or t.numel() < nbytes:
-            with on(stream):
-                t = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-            self._by_stream[ptr] = t
-        return t.data_ptr()
+            t = self._by_stream[ptr] = self._new(nbytes, stream)
+        return t
+
+    def _new(self, nbytes: int, stream) -> torch.Tensor:
+        with on(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+
+
+def address(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 def gptq_tokens_ld(cols: int) -> int:

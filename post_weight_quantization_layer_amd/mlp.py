@@ -59,6 +59,7 @@ class GatedMLP8:
             self._last = (t, r.dtype, R.gptq_gated_mlp_ws_bytes(self.block, r.dtype, t))
         n = self._last[2]
         r_out, h = self.outputs(t, r.dtype, stream)
-        R.gptq_gated_mlp_forward(self.block, r, gate, gate_tokens, r_out, h,
-                                 self.scratch(n, r, stream), n, stream)
+        ws = self.scratch(n, r, stream)
+        R.gptq_gated_mlp_forward(self.block, r, gate, gate_tokens, r_out, h, R.address(ws), n,
+                                 stream)
         return r_out, h

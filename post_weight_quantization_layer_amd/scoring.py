@@ -79,7 +79,7 @@ class TokenScorer:
         if self._last[0] != n:
             self._last = (n, R.gptq_token_logprobs_ws_bytes(n, self.vocab, self.top_k))
         nbytes = self._last[1]
+        ws = self.scratch(nbytes, logits, stream)
         R.gptq_token_logprobs(logits, ids, scale, self.top_k, out.logprob, out.rank, out.entropy,
-                              out.top_ids, out.top_logprobs,
-                              self.scratch(nbytes, logits, stream), nbytes, stream)
+                              out.top_ids, out.top_logprobs, R.address(ws), nbytes, stream)
         return out

@@ -116,7 +116,8 @@ class W8A8Linear:
         if y is None:
             y = self._new(tokens, x.dtype, stream)
         n = self._bytes("gptq_w8a8_linear_ws_bytes", tokens)
-        R.gptq_w8a8_linear(self.layer, x, y, self.scratch(n, self.mem, stream), n, stream)
+        ws = self.scratch(n, self.mem, stream)
+        R.gptq_w8a8_linear(self.layer, x, y, R.address(ws), n, stream)
         return y
 
     def product(self, tokens: TokenCodes, y: torch.Tensor | None = None,
@@ -130,6 +131,7 @@ class W8A8Linear:
         elif y.shape[0] != t:
             raise ValueError(f"y must have {t} rows, got {y.shape[0]}")
         n = self._bytes("gptq_w8a8_gemm_ws_bytes", t)
-        R.gptq_w8a8_gemm(self.layer, tokens.codes, tokens.scale, tokens.sum, y,
-                         self.scratch(n, self.mem, stream), n, stream)
+        ws = self.scratch(n, self.mem, stream)
+        R.gptq_w8a8_gemm(self.layer, tokens.codes, tokens.scale, tokens.sum, y, R.address(ws), n,
+                         stream)
         return y

@@ -1,0 +1,66 @@
+"""Captured calls of the running operators beside other calls of the same
+objects: a graph's replays give its results and write nothing else."""
+import numpy as np
+import pytest
+
+from tests.test_gpu_run import activations, layer_on_gpu, stored_layer, to_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+def linear(rng):
+    """Few tokens (rows kernel) and more (k in several parts): codes, scales, parts."""
+    lin = layer_on_gpu(*stored_layer(rng, 300, 4100))
+
+    def step(x):
+        return (lin(x),)
+    return step, 4100
+
+
+def scorer(rng):
+    import torch
+    from post_weight_quantization_layer_amd.scoring import TokenScorer
+    sc = TokenScorer(64, 30000, 7)
+
+    def step(x):
+        out = sc(x, torch.full((x.shape[0],), 5, device="cuda"))
+        return out.logprob, out.rank, out.entropy, out.top_ids, out.top_logprobs
+    return step, 30000
+
+
+MAKERS = [linear, scorer]
+
+
+@pytest.mark.parametrize("make", MAKERS)
+def test_replays_after_larger_calls_on_the_stream(make):
+    """Warm up and capture 2 tokens, then 40 and 64 on the same stream, then memory
+    for other tensors: the replays leave those as they are."""
+    import torch
+    rng = np.random.default_rng(41)
+    step, width = make(rng)
+    x = to_gpu(activations(rng, 2, width), "f16")
+    more = [to_gpu(activations(rng, t, width), "f16") for t in (40, 64)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = [t.clone() for t in step(x)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = step(x)
+        large = [[t.clone() for t in step(m)] for m in more]
+        # takes up whatever the stream's allocator has been given back
+        other = [torch.full((n,), 77, dtype=torch.uint8, device="cuda")
+                 for n in (512, 4096, 20000, 100000, 600000, 1 << 20) for _ in range(20)]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for t in got:
+            t.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+        assert all(bool((t == 77).all()) for t in other), i
+        with torch.cuda.stream(side):                  # eager calls go on as before
+            for m, w in zip(more, large):
+                assert all(torch.equal(a, b) for a, b in zip(step(m), w)), i
+        torch.cuda.synchronize()
