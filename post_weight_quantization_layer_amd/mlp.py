@@ -18,7 +18,7 @@ class GatedMLP8:
     """``enter``: the NormBlock before the block; ``gate_up``: gate and up
     stacked along the rows; ``leave``: the NormBlock after it (its ``pre`` norm
     is the next block's).  Calls on different streams may overlap: each stream
-    has its own outputs and scratch memory."""
+    has its own scratch memory."""
 
     def __init__(self, enter: NormBlock, gate_up: W8A8Linear, down: W8A8Linear,
                  leave: NormBlock):
@@ -30,24 +30,12 @@ class GatedMLP8:
         self.d, self.inner = down.rows, down.cols
         self.block = R.gptq_gated_mlp(enter.params, leave.params, gate_up.layer, down.layer)
         self.scratch = R.Scratch(down.device)
-        self._outputs: dict = {}
         self._last = (-1, None, 0)      # tokens, type, scratch bytes
 
-    def outputs(self, tokens: int, dtype: torch.dtype, stream) -> tuple:
-        """(r', h) of up to ``tokens`` tokens, one pair per stream and type."""
-        key = (R.stream_ptr(self.down.mem, stream), dtype)
-        kept = self._outputs.get(key)
-        if kept is None or kept[0].shape[0] < tokens:
-            with R.on(stream):
-                kept = tuple(torch.empty((tokens, self.d), dtype=dtype, device=self.down.device)
-                             for _ in range(2))
-            self._outputs[key] = kept
-        return kept if kept[0].shape[0] == tokens else tuple(t[:tokens] for t in kept)
-
     def __call__(self, r: torch.Tensor, *, gate=None, gate_tokens: int | None = None,
-                 stream=None):
-        """r: tokens x d; gate as for ``leave``.  Returns (r', h), which the next
-        call on the same stream overwrites."""
+                 r_out: torch.Tensor | None = None, h: torch.Tensor | None = None, stream=None):
+        """r: tokens x d; gate as for ``leave``.  Returns (r', h): ``r_out`` (which
+        may be r) and ``h``, or new tensors."""
         if r.dim() != 2 or r.shape[1] != self.d:
             raise ValueError(f"r must be tokens x {self.d}, got {tuple(r.shape)}")
         if not r.is_cuda:
@@ -58,7 +46,10 @@ class GatedMLP8:
         if self._last[:2] != (t, r.dtype):
             self._last = (t, r.dtype, R.gptq_gated_mlp_ws_bytes(self.block, r.dtype, t))
         n = self._last[2]
-        r_out, h = self.outputs(t, r.dtype, stream)
+        if r_out is None or h is None:
+            with R.on(stream):
+                r_out = torch.empty_like(r) if r_out is None else r_out
+                h = torch.empty_like(r) if h is None else h
         ws = self.scratch(n, r, stream)
         R.gptq_gated_mlp_forward(self.block, r, gate, gate_tokens, r_out, h, R.address(ws), n,
                                  stream)

@@ -3,7 +3,7 @@ objects: a graph's replays give its results and write nothing else."""
 import numpy as np
 import pytest
 
-from tests.test_gpu_run import activations, layer_on_gpu, stored_layer, to_gpu
+from tests.test_gpu_run import activations, layer_on_gpu, small_mlp, stored_layer, to_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -28,7 +28,11 @@ def scorer(rng):
     return step, 30000
 
 
-MAKERS = [linear, scorer]
+def gated_mlp(rng):
+    return small_mlp(rng)[0], 256
+
+
+MAKERS = [linear, scorer, gated_mlp]
 
 
 @pytest.mark.parametrize("make", MAKERS)
@@ -64,3 +68,30 @@ def test_replays_after_larger_calls_on_the_stream(make):
             for m, w in zip(more, large):
                 assert all(torch.equal(a, b) for a, b in zip(step(m), w)), i
         torch.cuda.synchronize()
+
+
+def test_gated_mlp_takes_its_own_outputs_and_others():
+    """An output goes on as an input, whole, in part or shifted by a row; outputs
+    of the caller's are written and returned, r' over r among them."""
+    import torch
+    rng = np.random.default_rng(43)
+    mlp, *_ = small_mlp(rng)
+    r0 = to_gpu(activations(rng, 30, 256), "f16")
+    r, h = mlp(r0)
+    kept = r.clone(), h.clone()
+    for part in (r, r[1:], r[3:20], h[2:]):
+        copy = part.clone()
+        got, want = mlp(part), mlp(copy)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.equal(part, copy)
+    assert torch.equal(r, kept[0]) and torch.equal(h, kept[1])
+    out, hout = torch.empty_like(r0), torch.empty((30, 300), dtype=r0.dtype, device="cuda")[:, 7:263]
+    got = mlp(r0, r_out=out, h=hout)
+    assert got[0] is out and got[1] is hout
+    assert torch.equal(out, kept[0]) and torch.equal(hout, kept[1])
+    got = mlp(r0, r_out=r0)
+    assert got[0] is r0 and torch.equal(r0, kept[0]) and torch.equal(got[1], kept[1])
+    with pytest.raises(ValueError):
+        mlp(r0, h=hout[1:])
+    with pytest.raises(TypeError):
+        mlp(r0, r_out=out.float())
