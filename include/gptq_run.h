@@ -171,8 +171,11 @@ typedef struct {
  *           used).
  *  gate     NULL (ones), or rows of d: token t takes row t / gate_tokens
  *           (gate_tokens = tokens: one row for all; 1: one per token).
- *  r_out    r', or NULL.  May be r itself.
- *  h        h in dtype, or NULL.  May be b itself.
+ *  r_out    r', or NULL.
+ *  h        h in dtype, or NULL.
+ *           Either may be r, b or gate itself (one row per token, the same
+ *           stride); otherwise its rows may not overlap any of those, nor each
+ *           other's: such calls are refused.
  *  codes, ld_codes, scale, sum  h as token codes, or codes NULL.
  * At least one of r_out, h and codes is given.
  */
@@ -209,7 +212,7 @@ size_t gptq_gated_mlp_ws_bytes(const gptq_gated_mlp *mlp, int32_t dtype,
  *  dtype     type of r, gate, r_out, h and the stored intermediates.  tokens
  *            <= 2^20, d <= 32768.
  *  gate      of leave, as in gptq_norm_block.
- *  r_out, h  as there; r_out may be r.  At least one is given.
+ *  r_out, h  as there; either may be r.  At least one is given.
  *  ws        scratch, 256-byte aligned, >= gptq_gated_mlp_ws_bytes.
  * On an error r_out and h are as before; ws may have been written.
  */

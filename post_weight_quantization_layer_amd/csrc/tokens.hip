@@ -11,6 +11,7 @@
 // 26 us, 4.3 TB/s.
 #include <algorithm>
 #include <string>
+#include <utility>
 
 #include "rows.h"
 
@@ -439,6 +440,37 @@ gptq_status check_codes(const int8_t *codes, int64_t ld_codes, int64_t cols, con
   return GPTQ_OK;
 }
 
+// Whether rows of `width` bytes, n of them `a_pitch` bytes apart from a on and m
+// `b_pitch` apart from b on, share a byte.  (Columns of one matrix do not.)
+bool rows_overlap(const void *a, uint64_t n, uint64_t a_pitch, const void *b, uint64_t m,
+                  uint64_t b_pitch, uint64_t width) {
+  if (reinterpret_cast<uintptr_t>(a) > reinterpret_cast<uintptr_t>(b))
+    return rows_overlap(b, m, b_pitch, a, n, a_pitch, width);
+  const uint64_t gap = reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a);
+  if (gap >= (n - 1) * a_pitch + width) return false;     // b begins after a's last row
+  uint64_t i = gap / a_pitch, j = 0;                      // the row of a that b begins in
+  if (a_pitch == b_pitch) {
+    const uint64_t at = gap % a_pitch;
+    return at < width || (at + width > a_pitch && i + 1 < n);
+  }
+  while (i < n && j < m) {                                // along both, row by row
+    const uint64_t x = i * a_pitch, y = gap + j * b_pitch;
+    if (x < y + width && y < x + width) return true;
+    if (x < y) ++i;
+    else ++j;
+  }
+  return false;
+}
+// An output's rows may be an input's (each is read before it is written) or share
+// nothing with it: rows that overlap others would be read and written by different
+// workgroups.
+bool clash(const void *out, int64_t ld_out, const void *in, int64_t ld_in, int64_t in_rows,
+           int64_t tokens, int64_t d, size_t e) {
+  if (!out || !in) return false;
+  if (out == in && in_rows == tokens && (ld_out == ld_in || tokens == 1)) return false;
+  return rows_overlap(out, tokens, ld_out * e, in, in_rows, ld_in * e, d * e);
+}
+
 // A launch has at most 2^32 threads, 1024 of them per row here.
 constexpr int64_t kMaxTokens = int64_t(1) << 21;
 
@@ -540,6 +572,17 @@ gptq_status gptq_norm_block(const gptq_norm_params *p, int32_t dtype, int64_t to
     if (r_out) GPTQ_TRY(check_activations(r_out, dtype, tokens, d, ld_r_out, "r_out"));
     if (h) GPTQ_TRY(check_activations(h, dtype, tokens, d, ld_h, "h"));
     if (codes) GPTQ_TRY(check_codes(codes, ld_codes, d, scale, sum));
+    const size_t e = type_bytes(dtype);
+    const int64_t gates = b && gate ? cdiv(tokens, std::min(gate_tokens, tokens)) : 0;
+    for (const auto &[out, ld_out] : {std::pair{r_out, ld_r_out}, std::pair{h, ld_h}})
+      if (clash(out, ld_out, r, ld_r, tokens, tokens, d, e) ||
+          clash(out, ld_out, b, ld_b, tokens, tokens, d, e) ||
+          (gates > 0 &&
+           clash(out, ld_out, gate, gates > 1 ? ld_gate : d, gates, tokens, d, e)))
+        return fail(GPTQ_ERR_INVALID_ARG, "r_out and h must be r, b or gate, row for row, or "
+                                          "overlap nothing of them");
+    if (r_out && h && rows_overlap(r_out, tokens, ld_r_out * e, h, tokens, ld_h * e, d * e))
+      return fail(GPTQ_ERR_INVALID_ARG, "r_out and h must not overlap");
     NormArgs a;
     a.r = r;
     a.b = b;
