@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import threading
 
 import torch
 
@@ -165,15 +166,20 @@ class Scratch:
 
     A call that is being captured gets a buffer of its own, from the graph's
     pool: the graph may be replayed after a larger call has replaced the stream's
-    buffer, or beside a call that uses it."""
+    buffer, or beside a call that uses it.
+
+    ``lock`` is held from asking for a buffer until the launches that use it are
+    issued, so that threads on one stream share its buffer call by call."""
 
     def __init__(self, device):
         self.device = device
+        self.lock = threading.Lock()
         self._by_stream: dict[int, torch.Tensor] = {}
 
     def __call__(self, nbytes: int, like: torch.Tensor, stream=None) -> torch.Tensor | None:
         """At least ``nbytes`` bytes for one call on ``stream`` (None: the current
-        stream of ``like``'s device), to be held until its launches are issued."""
+        stream of ``like``'s device), to be held, like ``lock``, until its launches
+        are issued."""
         if nbytes == 0:
             return None
         if capturing(stream):

@@ -18,7 +18,7 @@ class GatedMLP8:
     """``enter``: the NormBlock before the block; ``gate_up``: gate and up
     stacked along the rows; ``leave``: the NormBlock after it (its ``pre`` norm
     is the next block's).  Calls on different streams may overlap: each stream
-    has its own scratch memory."""
+    has its own scratch memory.  Threads may share it and a stream."""
 
     def __init__(self, enter: NormBlock, gate_up: W8A8Linear, down: W8A8Linear,
                  leave: NormBlock):
@@ -43,14 +43,16 @@ class GatedMLP8:
         R._dtype(r, "r")
         t = r.shape[0]
         gate_tokens = 1 if gate is None else tokens_per_gate(gate, gate_tokens, t)
-        if self._last[:2] != (t, r.dtype):
-            self._last = (t, r.dtype, R.gptq_gated_mlp_ws_bytes(self.block, r.dtype, t))
-        n = self._last[2]
+        last = self._last
+        if last[0] != t or last[1] is not r.dtype:
+            last = self._last = (t, r.dtype, R.gptq_gated_mlp_ws_bytes(self.block, r.dtype, t))
+        n = last[2]
         if r_out is None or h is None:
             with R.on(stream):
                 r_out = torch.empty_like(r) if r_out is None else r_out
                 h = torch.empty_like(r) if h is None else h
-        ws = self.scratch(n, r, stream)
-        R.gptq_gated_mlp_forward(self.block, r, gate, gate_tokens, r_out, h, R.address(ws), n,
-                                 stream)
+        with self.scratch.lock:
+            ws = self.scratch(n, r, stream)
+            R.gptq_gated_mlp_forward(self.block, r, gate, gate_tokens, r_out, h, R.address(ws), n,
+                                     stream)
         return r_out, h

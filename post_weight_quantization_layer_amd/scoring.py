@@ -39,7 +39,9 @@ class TokenLogprobs:
 
 class TokenScorer:
     """Owns the outputs and the scratch memory for up to ``rows`` rows of
-    ``vocab`` logits; a call's result is overwritten by the next."""
+    ``vocab`` logits; a call's result is overwritten by the next.  So calls of one
+    scorer follow each other: on one stream or ordered by events, and from one
+    thread at a time."""
 
     def __init__(self, rows: int, vocab: int, top_k: int = 0, device="cuda"):
         if not 0 <= top_k <= min(64, vocab):
@@ -76,10 +78,13 @@ class TokenScorer:
         else:
             R.vector(ids, "ids", n, torch.int64)
             out.ids = ids
-        if self._last[0] != n:
-            self._last = (n, R.gptq_token_logprobs_ws_bytes(n, self.vocab, self.top_k))
-        nbytes = self._last[1]
-        ws = self.scratch(nbytes, logits, stream)
-        R.gptq_token_logprobs(logits, ids, scale, self.top_k, out.logprob, out.rank, out.entropy,
-                              out.top_ids, out.top_logprobs, R.address(ws), nbytes, stream)
+        last = self._last
+        if last[0] != n:
+            last = self._last = (n, R.gptq_token_logprobs_ws_bytes(n, self.vocab, self.top_k))
+        nbytes = last[1]
+        with self.scratch.lock:
+            ws = self.scratch(nbytes, logits, stream)
+            R.gptq_token_logprobs(logits, ids, scale, self.top_k, out.logprob, out.rank,
+                                  out.entropy, out.top_ids, out.top_logprobs, R.address(ws),
+                                  nbytes, stream)
         return out

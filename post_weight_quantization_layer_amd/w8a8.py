@@ -68,7 +68,7 @@ def silu_mul_quantize(g: torch.Tensor, u: torch.Tensor, out: TokenCodes | None =
 
 class W8A8Linear:
     """A prepared per-row 8-bit layer.  Calls on different streams may overlap:
-    each stream has its own scratch memory."""
+    each stream has its own scratch memory.  Threads may share it and a stream."""
 
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor, stream=None):
         """codes rows x cols uint8; scale (float32) and zero (uint8) one per row."""
@@ -116,8 +116,9 @@ class W8A8Linear:
         if y is None:
             y = self._new(tokens, x.dtype, stream)
         n = self._bytes("gptq_w8a8_linear_ws_bytes", tokens)
-        ws = self.scratch(n, self.mem, stream)
-        R.gptq_w8a8_linear(self.layer, x, y, R.address(ws), n, stream)
+        with self.scratch.lock:
+            ws = self.scratch(n, self.mem, stream)
+            R.gptq_w8a8_linear(self.layer, x, y, R.address(ws), n, stream)
         return y
 
     def product(self, tokens: TokenCodes, y: torch.Tensor | None = None,
@@ -131,7 +132,8 @@ class W8A8Linear:
         elif y.shape[0] != t:
             raise ValueError(f"y must have {t} rows, got {y.shape[0]}")
         n = self._bytes("gptq_w8a8_gemm_ws_bytes", t)
-        ws = self.scratch(n, self.mem, stream)
-        R.gptq_w8a8_gemm(self.layer, tokens.codes, tokens.scale, tokens.sum, y, R.address(ws), n,
-                         stream)
+        with self.scratch.lock:
+            ws = self.scratch(n, self.mem, stream)
+            R.gptq_w8a8_gemm(self.layer, tokens.codes, tokens.scale, tokens.sum, y, R.address(ws),
+                             n, stream)
         return y

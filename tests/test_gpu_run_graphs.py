@@ -95,3 +95,27 @@ def test_gated_mlp_takes_its_own_outputs_and_others():
         mlp(r0, h=hout[1:])
     with pytest.raises(TypeError):
         mlp(r0, r_out=out.float())
+
+
+@pytest.mark.parametrize("make", [linear, gated_mlp])
+def test_threads_that_share_an_object_and_a_stream(make):
+    """Each thread's results are those of its own inputs."""
+    import threading
+    import torch
+    rng = np.random.default_rng(47)
+    step, width = make(rng)
+    xs = [to_gpu(activations(rng, t, width), "f16") for t in (1, 3, 20, 40)]
+    want = [[t.clone() for t in step(x)] for x in xs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        for _ in range(40):
+            if not all(torch.equal(a, b) for a, b in zip(step(xs[i]), want[i])):
+                wrong.append(i)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong

@@ -1,5 +1,8 @@
 """What the classes over gptq_run.h keep between calls, with the streams and the
 native calls replaced by stand-ins (no GPU)."""
+import threading
+import time
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -70,3 +73,56 @@ def test_a_block_calls_outputs_are_its_own(streams, monkeypatch):
         kept.append(mlp(torch.zeros(tokens, 4).as_subclass(OnGpu)))
     for i, (r, h) in enumerate(kept):
         assert (r == i).all() and (h == i).all() and len(r) == (2, 2, 3, 1)[i]
+
+
+class Issue:
+    """A native call of several launches: notes calls that use the same scratch at
+    once, and scratch smaller than asked for."""
+
+    def __init__(self):
+        self.busy, self.faults = set(), []
+
+    def __call__(self, ws, n, need):
+        if n < need:
+            self.faults.append(f"{n} bytes for {need}")
+        if ws in self.busy:
+            self.faults.append("two calls in one buffer")
+        self.busy.add(ws)
+        time.sleep(0.002)
+        self.busy.discard(ws)
+
+
+def from_threads(call, n=4, times=6):
+    def work(i):
+        for k in range(times):
+            call(1 + (i + k) % 3)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(n)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+
+
+def test_threads_on_one_stream_share_a_layer(streams, monkeypatch):
+    from post_weight_quantization_layer_amd.w8a8 import W8A8Linear
+    issue = Issue()
+    monkeypatch.setattr(R, "gptq_w8a8_linear_ws_bytes", lambda layer, t: 256 * t)
+    monkeypatch.setattr(R, "gptq_w8a8_linear",
+                        lambda layer, x, y, ws, n, stream: issue(ws, n, 256 * len(x)))
+    lin = W8A8Linear.__new__(W8A8Linear)
+    lin.rows, lin.cols, lin.device, lin.layer, lin._last = 4, 4, "cpu", None, {}
+    lin.mem, lin.scratch = torch.zeros(1), R.Scratch("cpu")
+    from_threads(lambda t: lin(torch.zeros(t, 4)))
+    assert not issue.faults
+
+
+def test_threads_on_one_stream_share_a_block(streams, monkeypatch):
+    issue = Issue()
+    mlp = gated_mlp(monkeypatch, lambda r_out, h, ws, n: issue(ws, n, 256 * len(h)))
+
+    def size(block, dtype, t):
+        time.sleep(0.001)
+        return 256 * t
+    monkeypatch.setattr(R, "gptq_gated_mlp_ws_bytes", size)
+    from_threads(lambda t: mlp(torch.zeros(t, 4).as_subclass(OnGpu)))
+    assert not issue.faults
