@@ -9,6 +9,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as B
+from . import binding_run as R
 
 
 def pack_zero_points(zero: torch.Tensor) -> torch.Tensor:
@@ -25,7 +26,9 @@ def pack_zero_points(zero: torch.Tensor) -> torch.Tensor:
 
 
 class W4A16Linear:
-    """Prepared layer plus the scratch of its products, on one device."""
+    """Prepared layer plus the scratch of its products, on one device.  Calls on
+    different streams may overlap, and threads may share it and a stream; a call
+    being captured into a graph has scratch of its own."""
 
     def __init__(self, packed: torch.Tensor, g_idx: torch.Tensor, scale: torch.Tensor,
                  zero_packed: torch.Tensor, rows: int, cols: int, group: int, stream=None):
@@ -36,7 +39,7 @@ class W4A16Linear:
                                           self.mem, stream)
         self.rows, self.cols = rows, cols
         self.device = dev
-        self.ws = None
+        self.scratch = R.Scratch(dev)
 
     @classmethod
     def from_codes(cls, codes: torch.Tensor, g_idx: torch.Tensor, scale: torch.Tensor,
@@ -48,17 +51,14 @@ class W4A16Linear:
         B.gptq_pack(codes, 4, packed, stream=stream)
         return cls(packed, g_idx, scale, pack_zero_points(zero), rows, cols, group, stream)
 
-    def workspace(self, batch: int) -> torch.Tensor | None:
-        n = B.gptq_w4a16_workspace_bytes(self.layer, batch)
-        if n == 0:
-            return None
-        if self.ws is None or self.ws.numel() < n:
-            self.ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-        return self.ws
+    def workspace(self, batch: int, stream=None) -> torch.Tensor | None:
+        """Scratch for a product on ``stream`` (None: the current one)."""
+        return self.scratch(B.gptq_w4a16_workspace_bytes(self.layer, batch), self.mem, stream)
 
     def __call__(self, x: torch.Tensor, y: torch.Tensor | None = None, stream=None):
         """x: batch x cols float16 -> y: batch x rows float16."""
         if y is None:
             y = torch.empty((x.shape[0], self.rows), dtype=torch.float16, device=x.device)
-        B.gptq_w4a16_gemm(self.layer, x, y, self.workspace(x.shape[0]), stream=stream)
+        with self.scratch.lock:
+            B.gptq_w4a16_gemm(self.layer, x, y, self.workspace(x.shape[0], stream), stream=stream)
         return y

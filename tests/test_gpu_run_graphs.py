@@ -1,4 +1,4 @@
-"""Captured calls of the running operators beside other calls of the same
+"""Captured calls of the classes that run layers beside other calls of the same
 objects: a graph's replays give its results and write nothing else."""
 import numpy as np
 import pytest
@@ -32,7 +32,22 @@ def gated_mlp(rng):
     return small_mlp(rng)[0], 256
 
 
-MAKERS = [linear, scorer, gated_mlp]
+def w4a16(rng):
+    """Columns stored out of order: x is gathered into scratch before the product."""
+    import torch
+    from post_weight_quantization_layer_amd import inputs as I
+    from post_weight_quantization_layer_amd.w4a16 import W4A16Linear
+    st = I.stored_int4_layer(512, 2048, 128, True, seed=7)
+    lin = W4A16Linear.from_codes(*(torch.from_numpy(a).cuda()
+                                   for a in (st.codes, st.g_idx, st.scale, st.zero)), 128)
+    assert lin.workspace(2) is not None
+
+    def step(x):
+        return (lin(x),)
+    return step, 2048
+
+
+MAKERS = [linear, scorer, gated_mlp, w4a16]
 
 
 @pytest.mark.parametrize("make", MAKERS)
@@ -97,7 +112,7 @@ def test_gated_mlp_takes_its_own_outputs_and_others():
         mlp(r0, r_out=out.float())
 
 
-@pytest.mark.parametrize("make", [linear, gated_mlp])
+@pytest.mark.parametrize("make", [linear, gated_mlp, w4a16])
 def test_threads_that_share_an_object_and_a_stream(make):
     """Each thread's results are those of its own inputs."""
     import threading

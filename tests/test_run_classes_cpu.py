@@ -126,3 +126,26 @@ def test_threads_on_one_stream_share_a_block(streams, monkeypatch):
     monkeypatch.setattr(R, "gptq_gated_mlp_ws_bytes", size)
     from_threads(lambda t: mlp(torch.zeros(t, 4).as_subclass(OnGpu)))
     assert not issue.faults
+
+
+def test_a_4_bit_layers_scratch(streams, monkeypatch):
+    """Per stream, call by call, and none of a captured call's."""
+    from post_weight_quantization_layer_amd import binding as B
+    from post_weight_quantization_layer_amd.w4a16 import W4A16Linear
+    issue = Issue()
+    monkeypatch.setattr(B, "gptq_w4a16_workspace_bytes", lambda layer, t: 256 * t)
+    monkeypatch.setattr(B, "gptq_w4a16_gemm", lambda layer, x, y, ws, stream=None:
+                        issue(ws.data_ptr(), ws.numel(), 256 * len(x)))
+    monkeypatch.setattr(B, "gptq_w4a16_layer_bytes", lambda *a: 256)
+    monkeypatch.setattr(B, "gptq_w4a16_prepare", lambda *a: None)
+    none = torch.zeros(1)
+    lin = W4A16Linear(none, none, none, none, 4, 4, 4)
+    from_threads(lambda t: lin(torch.zeros(t, 4)))
+    assert not issue.faults
+    one = lin.workspace(3)
+    streams.stream = 2
+    assert lin.workspace(3).data_ptr() != one.data_ptr()
+    streams.capturing = True
+    caught = lin.workspace(3)
+    streams.capturing = False
+    assert lin.workspace(3) is not caught
