@@ -58,7 +58,8 @@ class W4A16Linear:
     def __call__(self, x: torch.Tensor, y: torch.Tensor | None = None, stream=None):
         """x: batch x cols float16 -> y: batch x rows float16."""
         if y is None:
-            y = torch.empty((x.shape[0], self.rows), dtype=torch.float16, device=x.device)
+            with R.on(stream):
+                y = torch.empty((x.shape[0], self.rows), dtype=torch.float16, device=x.device)
         with self.scratch.lock:
             B.gptq_w4a16_gemm(self.layer, x, y, self.workspace(x.shape[0], stream), stream=stream)
         return y

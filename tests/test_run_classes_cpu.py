@@ -1,5 +1,6 @@
 """What the classes over gptq_run.h keep between calls, with the streams and the
 native calls replaced by stand-ins (no GPU)."""
+import contextlib
 import threading
 import time
 
@@ -149,3 +150,12 @@ def test_a_4_bit_layers_scratch(streams, monkeypatch):
     caught = lin.workspace(3)
     streams.capturing = False
     assert lin.workspace(3) is not caught
+    # the output it allocates belongs to the stream it is written on
+    asked = []
+
+    def on(stream):
+        asked.append(stream)
+        return contextlib.nullcontext()
+    monkeypatch.setattr(R, "on", on)
+    lin(torch.zeros(3, 4), stream="side")
+    assert asked == ["side"]
