@@ -128,6 +128,14 @@ def matrix(t: torch.Tensor, what: str, rows: int | None = None, cols: int | None
     return t.data_ptr(), stride[0] if r > 1 else c    # torch may report any for one row or none
 
 
+def on_gpu(device, what: str) -> torch.device:
+    """The device of buffers that kernels write."""
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError(f"{what} must be on the GPU, not on {device}")
+    return device
+
+
 def ld(t: torch.Tensor) -> int:
     """Row stride; a single row's is its length (torch may report any)."""
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]

@@ -46,6 +46,7 @@ class TokenScorer:
     def __init__(self, rows: int, vocab: int, top_k: int = 0, device="cuda"):
         if not 0 <= top_k <= min(64, vocab):
             raise ValueError("top_k must be in [0, min(64, vocab)]")
+        device = R.on_gpu(device, "a scorer's outputs")
         self.rows, self.vocab, self.top_k = rows, vocab, top_k
 
         def buffer(dtype, *shape):

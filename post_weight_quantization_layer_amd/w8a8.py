@@ -16,6 +16,7 @@ class TokenCodes:
     sum per token: up to ``tokens`` rows of ``cols`` features."""
 
     def __init__(self, tokens: int, cols: int, device="cuda", stream=None):
+        device = R.on_gpu(device, "token codes")
         self.tokens, self.cols = tokens, cols
         with R.on(stream):
             self.codes = torch.empty((tokens, R.gptq_tokens_ld(cols)), dtype=torch.int8,

@@ -159,3 +159,14 @@ def test_a_4_bit_layers_scratch(streams, monkeypatch):
     monkeypatch.setattr(R, "on", on)
     lin(torch.zeros(3, 4), stream="side")
     assert asked == ["side"]
+
+
+def test_buffers_off_the_gpu_are_refused():
+    """Kernels would write to host addresses."""
+    from post_weight_quantization_layer_amd.scoring import TokenScorer
+    from post_weight_quantization_layer_amd.w8a8 import TokenCodes
+    for device in ("cpu", torch.device("cpu"), "meta"):
+        with pytest.raises(ValueError, match="GPU"):
+            TokenCodes(4, 8, device)
+        with pytest.raises(ValueError, match="GPU"):
+            TokenScorer(4, 8, 2, device=device)
