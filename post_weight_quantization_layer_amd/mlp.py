@@ -52,6 +52,8 @@ class GatedMLP8:
                 r_out = torch.empty_like(r) if r_out is None else r_out
                 h = torch.empty_like(r) if h is None else h
         with self.scratch.lock:
+            # the struct holds copies: what the norms say now counts
+            self.block.enter, self.block.leave = self.enter.params, self.leave.params
             ws = self.scratch(n, r, stream)
             R.gptq_gated_mlp_forward(self.block, r, gate, gate_tokens, r_out, h, R.address(ws), n,
                                      stream)

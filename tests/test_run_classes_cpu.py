@@ -170,3 +170,16 @@ def test_buffers_off_the_gpu_are_refused():
             TokenCodes(4, 8, device)
         with pytest.raises(ValueError, match="GPU"):
             TokenScorer(4, 8, 2, device=device)
+
+
+def test_a_block_uses_its_norms_as_they_are(streams, monkeypatch):
+    """A change of a norm's parameters reaches the block it was made with."""
+    mlp = gated_mlp(monkeypatch, None)
+    scales = []
+    monkeypatch.setattr(R, "gptq_gated_mlp_forward", lambda block, *rest: scales.append(
+        (block.enter.residual_scale, block.leave.residual_scale)))
+    r = torch.zeros(2, 4).as_subclass(OnGpu)
+    for scale in (0.5, 0.75):
+        mlp.enter.params.residual_scale = scale
+        mlp(r)
+    assert scales == [(0.5, 0.5), (0.75, 0.75)]      # one norm object on both sides here
