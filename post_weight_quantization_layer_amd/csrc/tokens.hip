@@ -52,15 +52,21 @@ __device__ __forceinline__ void store_codes(const float v[NCH][8], int lane, int
   }
 }
 
-// g / (1 + e^-g) within about 6 ulp: e^-g as a power of two whose argument's
-// rounding error is put back (it would be |g| ulp), and a reciprocal instead of
-// a division; at -infinity and +infinity the quotient's own limits.
+// g / (1 + e^-g) within 7 u (u = 2^-24): e^-g as a power of two (2 u) whose
+// argument's rounding error is put back (u; it would be |g| ulp), the sum (u), and
+// a reciprocal (2 u) and a product (u) instead of a division.  From |g| = 83 on the 1
+// or the exponential no longer counts; g e^g is formed with e^(g/2) twice, since
+// e^-g overflows and e^g loses bits before g e^g does.  +infinity stays, -infinity
+// gives the quotient's NaN.
 __device__ __forceinline__ float silu(float g) {
   const float t = g * -1.4426950408889634f;
   const float lo = __builtin_fmaf(g, -1.4426950408889634f, -t) - g * 1.9259629911266175e-8f;
   const float e = __builtin_amdgcn_exp2f(t);
   const float r = g * __builtin_amdgcn_rcpf(1.f + __builtin_fmaf(e, lo * 0.6931471805599453f, e));
-  return fabsf(t) < 120.f ? r : g > 0.f ? g : g / (1.f + expf(-g));
+  if (fabsf(t) < 120.f) return r;
+  if (g > 0.f) return g;
+  const float h = expf(0.5f * g);
+  return g * h * h;
 }
 
 struct CodesOut {
