@@ -627,14 +627,15 @@ size_t part_bytes(const Geometry &g, int64_t tokens, const Plan &p) {
                   (32 * p.fa * 32 * p.fb * sizeof(int32_t)));
 }
 
+// Launch names tell the tile: rows x tokens.
 template <int FA, int FB, int DEPTH, bool SPLIT>
-gptq_status launch_tiles(const GemmArgs &a, int splits, hipStream_t s) {
+gptq_status launch_tiles(const char *name, const GemmArgs &a, int splits, hipStream_t s) {
   auto kern = w8a8_tile_kernel<FA, FB, DEPTH, SPLIT>;
   const size_t lds = size_t(2) * 32 * (FA + FB) * kStep;
   GPTQ_TRY(allow_dynamic_lds(reinterpret_cast<const void *>(kern), lds));
   const int rt = int(cdiv(a.rows, 32 * FA)), tt = int(cdiv(a.tokens, 32 * FB));
   const uint32_t tiles = uint32_t(rt) * uint32_t(tt);
-  GPTQ_TRY(launch("w8a8_gemm", kern, dim3(tiles * splits), dim3(256), lds, s, a, tt, rt, splits));
+  GPTQ_TRY(launch(name, kern, dim3(tiles * splits), dim3(256), lds, s, a, tt, rt, splits));
   if constexpr (SPLIT)
     GPTQ_TRY(launch("w8a8_join", w8a8_join_kernel<FA, FB>, dim3(tiles * FA), dim3(256), 0, s, a, tt,
                     rt, splits));
@@ -666,13 +667,13 @@ gptq_status gemm_launch(const gptq_w8a8_layer *l, const int8_t *codes, int64_t l
   if (p.rows)
     return launch("w8a8_rows", tokens <= 16 ? w8a8_rows_kernel<1> : w8a8_rows_kernel<2>,
                   dim3(uint32_t(a.row_tiles)), dim3(64 * kRowsWaves), 0, s, a);
-  if (p.fa == 8) return launch_tiles<8, 8, 1, false>(a, 1, s);
-  if (p.fb == 8) return launch_tiles<4, 8, 1, false>(a, 1, s);
+  if (p.fa == 8) return launch_tiles<8, 8, 1, false>("w8a8_gemm_256x256", a, 1, s);
+  if (p.fb == 8) return launch_tiles<4, 8, 1, false>("w8a8_gemm_128x256", a, 1, s);
   if (p.fb == 2)
-    return p.splits > 1 ? launch_tiles<4, 2, 3, true>(a, p.splits, s)
-                        : launch_tiles<4, 2, 3, false>(a, 1, s);
-  return p.splits > 1 ? launch_tiles<4, 4, 2, true>(a, p.splits, s)
-                      : launch_tiles<4, 4, 2, false>(a, 1, s);
+    return p.splits > 1 ? launch_tiles<4, 2, 3, true>("w8a8_gemm_128x64_split", a, p.splits, s)
+                        : launch_tiles<4, 2, 3, false>("w8a8_gemm_128x64", a, 1, s);
+  return p.splits > 1 ? launch_tiles<4, 4, 2, true>("w8a8_gemm_128x128_split", a, p.splits, s)
+                      : launch_tiles<4, 4, 2, false>("w8a8_gemm_128x128", a, 1, s);
 }
 
 }  // namespace
