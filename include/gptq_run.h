@@ -191,8 +191,8 @@ gptq_status gptq_norm_block(const gptq_norm_params *p, int32_t dtype,
 /* --------------------------------------------------------- gated MLP block
  * With an input r of the residual stream (tokens x d):
  *
- *   x = codes(N_pre(r))             enter (its pre norm; r is scaled by its
- *                                   residual_scale)
+ *   x = codes(N_pre(r))             enter (its pre norm, of r scaled by its
+ *                                   residual_scale; leave takes r as it is)
  *   g, u = the halves of x W_gu^T   gate_up, 2 inner x d, rounded to dtype
  *   b = codes(silu(g) u) W_d^T      down, d x inner, rounded to dtype
  *   r', h                           leave, of r and b

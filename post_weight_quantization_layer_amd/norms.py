@@ -47,10 +47,12 @@ class NormBlock:
         """r, b: tokens x d.  gate: rows of d, ``gate_tokens`` consecutive tokens
         each (default: one row for all tokens, else one per token).
 
-        Returns (r', h).  r' goes to ``r_out`` (which may be r; allocated if
-        None and b is given, not written if None and b is None).  h goes to
-        ``h`` and / or, as codes, to ``codes``; the second result is ``codes``
-        where only that is given, and a new tensor where neither is."""
+        Returns (r', h).  r' goes to ``r_out`` (which may be r), or to a new
+        tensor if b is given.  With neither, r' is not stored: the first result
+        is r itself, not scaled by ``residual_scale`` (h is made from the scaled
+        one).  h goes to ``h`` and / or, as codes, to ``codes``; the second result
+        is ``codes`` where only that is given, and a new tensor where neither
+        is."""
         shape = r.shape
         if len(shape) != 2 or shape[1] != self.d:
             raise ValueError(f"r must be tokens x {self.d}, got {tuple(shape)}")
