@@ -37,6 +37,7 @@ constexpr int kUnroll = 2;
 constexpr int kTile = kUnroll * kChunkElems;
 constexpr int kMaxTop = 64;
 constexpr int kGroups = 32;                 // groups of tiles with a maximum of their own
+typedef uint16_t __attribute__((may_alias)) group_max_t;   // shares LDS with the lists' keys
 constexpr int kUncut = 64;                  // shorter lists are not cut before the last step
 // A wave's list is cut to k once it is longer than 2 k + 32, before the next
 // entry is added; so it takes a chunk (512) on top of that.
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kThreads) score_kernel(ScoreArgs a) {
   uint64_t *list = lists + (TOP ? wave * kListCap : 0);
   // The group maxima of a wave lie where its list will be.
   static_assert(kGroups * 64 * 2 <= kListCap * 8, "");
-  uint16_t *group_max = reinterpret_cast<uint16_t *>(list) + lane;
+  group_max_t *group_max = reinterpret_cast<group_max_t *>(list) + lane;
   int n = 0;                       // list length (wave-uniform)
   float thr = -INFINITY;           // candidates are > thr
   const int limit = 2 * a.k + kListSlack;
