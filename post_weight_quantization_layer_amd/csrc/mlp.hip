@@ -1,7 +1,8 @@
 // A gated MLP block on per-row 8-bit layers as one call: the five launches of
 // its operators, one after the other on the stream.  Issued from one place
 // because for few tokens the host's work between them is the block's time (2
-// tokens, 1024 x 1651: 40 us as five calls from Python, 19 us as one).
+// tokens, 1024 x 1651: 36 us as five calls from Python, 24 us as one, 21 us with
+// outputs of the caller's).
 #include <algorithm>
 #include <string>
 

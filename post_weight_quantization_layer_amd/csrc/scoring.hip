@@ -3,10 +3,11 @@
 //
 // With c = scale log2 e, every lane keeps a running maximum m of its logits,
 // s = sum 2^(c l - M) and t = sum (c l - M) 2^(c l - M), M being the float
-// nearest c m (c m itself from 2^22 up); lanes, waves and, when a row is split over workgroups, parts
-// are joined by rescaling to the common maximum.  Then ln p = ln 2 (c l - M) -
-// ln s and the entropy is ln s - ln 2 t / s.  c l - M is one fused operation,
-// exact up to its last rounding because M, not c m, is the reference.
+// nearest c m (c m itself from 2^22 up); lanes, waves and, when a row is split
+// over workgroups, parts are joined by rescaling to the common maximum.  Then
+// ln p = ln 2 (c l - M) - ln s and the entropy is ln s - ln 2 t / s.  c l - M is
+// one fused operation, exact up to its last rounding because M, not c m, is the
+// reference.
 //
 // Alternatives: the pass keeps each lane's maximum over groups of tiles, in
 // LDS.  After it, the k-th largest of the 256 lanes' own maxima is a threshold

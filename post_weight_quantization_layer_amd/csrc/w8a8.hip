@@ -204,11 +204,14 @@ __device__ __forceinline__ void lds_barrier() {
 // Small tiles, whose stages are shorter than a memory access, take DEPTH 2
 // or 3; 256 x 256 tiles have registers for 1.
 //
-// 8192 x 28672 x 8192: 1.46-1.55 ms, 2.5-2.6 POP/s (a library product of the
-// same sizes 1.90 ms).  The matrix units are then 62 % busy at 1.87 GHz of
-// 2.4; with every load from memory left out it gained 11 %, so the card's
-// power bounds it.  16 x 28672 x 8192: 44 us, its 236 MB at 5.4 TB/s.  333 x
-// 4091 x 4100: 16 us, bound by the tiles' traffic from L2.
+// 8192 x 28672 x 8192: 1.43-1.55 ms, 2.5-2.7 POP/s (a library product of the
+// same sizes 1.90 ms).  It takes 2.98 M cycles, in 62 % of which the matrix units
+// are busy; with every load from memory left out it gained 11 %.  The clock under
+// it was 1.64 to 1.91 GHz of 2.4, and the time goes with it.  16 x 28672 x 8192: 44
+// us, its 236 MB at 5.4 TB/s.  333 x 4091 x 4100: 16 us, by latency: 192 workgroups
+// leave 64 compute units idle, and in the others, with a wave per SIMD, the matrix
+// units are busy 24 % of the time; a wave waits for data or a barrier in 26 % of
+// its cycles and to issue in 25 %.  (L2 gives 159 MB, 49 bytes per ns and unit.)
 __device__ __forceinline__ int swz(int r) { return (r >> 1) & 7; }
 
 // Tiles in bands of kBand token tiles, tokens fastest: workgroups are dealt
@@ -228,8 +231,10 @@ __device__ __forceinline__ void tile_at(int bid, int tt, int rt, int &t, int &r)
 // builtin leaves the result's register free; with every accumulation register
 // taken, the compiler then moved whole accumulators between files in the
 // loop.)  The operands come from LDS reads, never straight from vector ALU
-// instructions, and acc is next touched 16 or more of these later; after the
-// last one, and before the first, settle() waits the pipeline out.
+// instructions.  An acc is next touched FA FB of these later (8 in the smallest
+// tiles, at 16 cycles each), and then only as the accumulator of the same
+// instruction, which the matrix unit orders by itself.  After the last one, and
+// before the first, settle() waits the pipeline out.
 __device__ __forceinline__ void mfma_acc(i32x4_t &acc, i32x4_t w, i32x4_t x) {
   asm("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(w), "v"(x));
 }
