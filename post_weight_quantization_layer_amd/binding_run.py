@@ -184,6 +184,9 @@ class Scratch:
         self.lock = threading.Lock()
         self._by_stream: dict[int, torch.Tensor] = {}
 
+    def __reduce__(self):
+        return Scratch, (self.device,)      # a copy has a lock and buffers of its own
+
     def __call__(self, nbytes: int, like: torch.Tensor, stream=None) -> torch.Tensor | None:
         """At least ``nbytes`` bytes for one call on ``stream`` (None: the current
         stream of ``like``'s device), to be held, like ``lock``, until its launches

@@ -183,3 +183,14 @@ def test_a_block_uses_its_norms_as_they_are(streams, monkeypatch):
         mlp.enter.params.residual_scale = scale
         mlp(r)
     assert scales == [(0.5, 0.5), (0.75, 0.75)]      # one norm object on both sides here
+
+
+def test_scratch_of_a_copied_object(streams):
+    import copy
+    import pickle
+    s, like = R.Scratch(torch.device("cpu")), torch.zeros(1)
+    kept = s(100, like)
+    for twin in (copy.deepcopy(s), pickle.loads(pickle.dumps(s))):
+        assert twin.device == s.device and twin.lock is not s.lock
+        assert twin(100, like).data_ptr() != kept.data_ptr()
+    assert s(100, like) is kept
