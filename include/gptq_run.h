@@ -65,9 +65,9 @@ gptq_status gptq_quantize_tokens(const void *x, int32_t x_dtype, int64_t tokens,
                                  int64_t ld_codes, float *scale, int32_t *sum,
                                  void *stream);
 
-/* The same of x = silu(g) * u, silu(g) = g / (1 + e^-g) (NaN for g = -infinity),
- * which is not rounded in between.  g and u have dtype `dtype` and row stride ld (they may be the
- * two halves of one matrix). */
+/* The same of x = silu(g) * u, silu(g) = g / (1 + e^-g) (NaN for g =
+ * -infinity), which is not rounded in between.  g and u have dtype `dtype` and
+ * row stride ld (they may be the two halves of one matrix). */
 gptq_status gptq_silu_mul_quantize(const void *g, const void *u, int32_t dtype,
                                    int64_t tokens, int64_t cols, int64_t ld,
                                    int8_t *codes, int64_t ld_codes,

@@ -84,10 +84,10 @@ __device__ __forceinline__ float key_value(uint64_t key) { return from_ordered(u
 __device__ __forceinline__ int key_index(uint64_t key) { return int(~uint32_t(key)); }
 
 // c l - M for a row maximum m.  M is off c m by up to half a unit in its last
-// place, which every difference to it carries and the sums' scale with them: 1/4
-// below kLarge, harmless, but beyond 2^7 powers of two of such differences leave
-// float32 (a lane that has seen nothing but masks of -1e10).  From kLarge up the
-// sums are relative to c m itself: c (l - m), halved against overflow.
+// place, and the sums are off by 2 to that power until they are joined: nothing
+// below kLarge, where it is 1/8 at most, but past float32 for a lane that has seen
+// only masks of -1e10, where it is hundreds.  From kLarge up the sums are relative
+// to c m itself: c (l - m), halved against overflow.
 constexpr float kLarge = 4194304.f;
 // M: the product rounded, never fused into what uses it.
 __device__ __forceinline__ float reference(float m, float c) {
