@@ -1059,9 +1059,9 @@ BlockWs block_ws(const gptq_f8_ff *f, int64_t tokens, void *mem) {
     at += half == kFew ? one : 2 * one;
   }
   w.parts = reinterpret_cast<void *>(base + at);
-  if (half != kFew)
-    at += std::max(half == kApart ? part_bytes(geometry(f->gate.rows, f->gate.cols), tokens, 2) : 0,
-                   part_bytes(geometry(f->down.rows, f->down.cols), tokens, 1));
+  // The down product is planned on its own: wide ones of few tokens are split too.
+  at += std::max(half == kApart ? part_bytes(geometry(f->gate.rows, f->gate.cols), tokens, 2) : 0,
+                 part_bytes(geometry(f->down.rows, f->down.cols), tokens, 1));
   w.bytes = at;
   return w;
 }

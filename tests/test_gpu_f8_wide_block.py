@@ -1,0 +1,35 @@
+"""The block on 8-bit floats where few tokens meet a wide down product, whose k is split: what
+it writes stays within the scratch it asks for."""
+import pytest
+
+from tests.test_gpu_f8 import U, block_reference, launched, make, stored
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("t,d,n", [(5, 32896, 11008), (16, 40960, 14336)])
+def test_few_tokens_of_a_wide_block(t, d, n):
+    """The memory behind the scratch stays as it was.  The result's tolerance is that of
+    test_gpu_f8's blocks with sums to 32 bits: v is off by e = (blocks + 12) 2^-24 of its size at
+    most, codes by 2^-3 sqrt(16 e) of the norm, with 320 blocks 2.3e-3; the down product adds
+    4e-5."""
+    import torch
+    from post_weight_quantization_layer_amd import binding_ff as F
+    from post_weight_quantization_layer_amd.f8 import F8Linear
+    layers = [stored(i + d, *shape) for i, shape in enumerate(((n, d), (n, d), (d, n)))]
+    lins = [F8Linear(c, s) for c, s, _ in layers]
+    block = F.gptq_f8_ff(*(lin.layer for lin in lins))
+    x = make(t, t, d, "f16")
+    y = torch.empty_like(x)
+    need, guard = F.gptq_f8_ff_ws_bytes(block, t), 1 << 26
+    ws = torch.full((need + guard,), 0x5a, dtype=torch.uint8, device="cuda")
+    print("wide block", t, d, n, "scratch", need, flush=True)
+    names = launched(lambda: F.gptq_f8_ff_forward(block, x, y, ws.data_ptr(), need))
+    assert "f8_rows_gate_up" in names
+    if torch.cuda.get_device_properties(0).multi_processor_count == 256:
+        assert {"f8_gemm_128x64", "f8_join"} <= names
+    assert bool((ws[need:] == 0x5a).all())
+    want = block_reference(x, layers)
+    e = (d / 128 + 12) * 2.0 ** -24
+    off = 2.0 ** -3 * (16 * e) ** 0.5 + 4e-5
+    assert (y.double() - want).norm() / want.norm() <= U["f16"] + off
