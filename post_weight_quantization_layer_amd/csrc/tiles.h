@@ -49,17 +49,19 @@ __device__ __forceinline__ void tile_at(int bid, int tt, int rt, int &t, int &r)
 // tell one buffer in LDS from another, would wait for all such copies before every read.
 // It does not count them, so it must not have to wait for a load of its own while some are
 // on their way: that would be a wait for every copy asked for before the load.
+// A load that writes LDS needs a wait state after a scalar write of M0; the compiler, which
+// puts it before its own, does not look into assembly.
 __device__ __forceinline__ void copy16_to_lds(const uint8_t *base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :: "s"(lds), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void copy4_to_lds(const uint8_t *base, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                :: "s"(lds), "v"(off), "s"(base) : "memory");
 }
 // The same from each lane's own address.
 __device__ __forceinline__ void copy16_to_lds(const void *from, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :: "s"(lds), "v"(from) : "memory");
 }
 // All but this wave's last N copies have landed.
