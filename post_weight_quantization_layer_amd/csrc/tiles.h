@@ -53,16 +53,16 @@ __device__ __forceinline__ void tile_at(int bid, int tt, int rt, int &t, int &r)
 // puts it before its own, does not look into assembly.
 __device__ __forceinline__ void copy16_to_lds(const uint8_t *base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :: "s"(lds), "v"(off), "s"(base) : "memory");
+               :: "s"(lds), "v"(off), "s"(base) : "m0", "memory");
 }
 __device__ __forceinline__ void copy4_to_lds(const uint8_t *base, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-               :: "s"(lds), "v"(off), "s"(base) : "memory");
+               :: "s"(lds), "v"(off), "s"(base) : "m0", "memory");
 }
 // The same from each lane's own address.
 __device__ __forceinline__ void copy16_to_lds(const void *from, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-               :: "s"(lds), "v"(from) : "memory");
+               :: "s"(lds), "v"(from) : "m0", "memory");
 }
 // All but this wave's last N copies have landed.
 template <int N>

@@ -1,6 +1,6 @@
 """The loads that write LDS past the registers (tiles.h), as they are assembled: the register
 that holds their address in LDS is written by a scalar instruction, after which such a load
-needs one wait state (no GPU)."""
+needs one wait state, and the compiler has to know that it changed (no GPU)."""
 import os
 import re
 import shutil
@@ -69,3 +69,11 @@ def test_a_wait_state_between_the_address_and_the_load(instructions, name, loads
     assert len(at) == loads
     for i in at:
         assert not writes_m0(lines[i - 1]), lines[i - 1:i + 1]
+
+
+def test_the_compiler_sets_its_own_address_again(instructions):
+    """Between a copy and the compiler's next load of that kind, which writes elsewhere."""
+    lines = instructions["beside"]
+    at = [i for i, line in enumerate(lines) if re.match(r"global_load_lds_", line)]
+    for before, load in zip([0] + at, at):
+        assert any(writes_m0(line) for line in lines[before:load]), lines[before:load + 1]
