@@ -167,6 +167,9 @@ def gptq_f8_ff_forward(ff: gptq_f8_ff, x, y, ws: int | None = None, ws_bytes: in
                                       R.stream_ptr(x, stream)))
 
 
+_KINDS = {code: kind for kind, code in R.DTYPES.items()}
+
+
 def make_ff(gate, up, down) -> gptq_ff:
     """The weights of a block: gate and up inner x d, down d x inner, of one type."""
     gptr, gld = R.matrix(gate, "gate")
@@ -189,8 +192,9 @@ def gptq_ff_backward_ws_bytes(ff: gptq_ff, tokens: int) -> int:
 
 
 def gptq_ff_forward(ff: gptq_ff, x, y, saved=None, ws=None, stream=None):
-    """x tokens x d; y a new tokens x d matrix; saved, ws: byte tensors or None."""
-    ptr, stride = R.matrix(x, "x", None, ff.d)
+    """x tokens x d, of the weights' type; y a new tokens x d matrix; saved, ws: byte tensors or
+    None."""
+    ptr, stride = R.matrix(x, "x", None, ff.d, _KINDS[ff.dtype])
     R._check((_lib or lib()).gptq_ff_forward(
         ff, ptr, stride, x.shape[0], y.data_ptr(), ff.d, R.address(saved),
         0 if saved is None else saved.numel(), R.address(ws), 0 if ws is None else ws.numel(),
@@ -199,8 +203,8 @@ def gptq_ff_forward(ff: gptq_ff, x, y, saved=None, ws=None, stream=None):
 
 def gptq_ff_backward(ff: gptq_ff, x, saved, dy, dx=None, dgate=None, dup=None, ddown=None,
                      ws=None, stream=None):
-    """dx, dgate, dup, ddown: new matrices to write, or None."""
-    ptr, stride = R.matrix(x, "x", None, ff.d)
+    """x, dy of the weights' type; dx, dgate, dup, ddown: new matrices to write, or None."""
+    ptr, stride = R.matrix(x, "x", None, ff.d, _KINDS[ff.dtype])
     dptr, dstride = R.matrix(dy, "dy", x.shape[0], ff.d, x.dtype)
     d, inner, at = ff.d, ff.inner, R.address
     R._check((_lib or lib()).gptq_ff_backward(

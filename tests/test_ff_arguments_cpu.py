@@ -1,0 +1,71 @@
+"""What the calls of the 16-bit feed-forward block refuse before they reach the library (no
+GPU: tensors that say they are on one, and a library that must not be called)."""
+import contextlib
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from post_weight_quantization_layer_amd import binding_ff as F
+from post_weight_quantization_layer_amd import feed_forward as FF
+
+
+class OnGpu(torch.Tensor):
+    is_cuda = True
+
+
+
+def on_gpu(*shape, dtype):
+    return torch.zeros(shape).to(dtype).as_subclass(OnGpu)
+
+
+class Library:
+    """Sizes that are plausible; calls that are counted."""
+
+    def __init__(self):
+        self.calls = 0
+
+    def __getattr__(self, name):
+        def call(*args):
+            if not name.endswith("_bytes"):
+                self.calls += 1
+            return 1 << 16 if name.endswith("_bytes") else 0
+        return call
+
+
+@pytest.fixture
+def library(monkeypatch):
+    lib = Library()
+    monkeypatch.setattr(F, "_lib", lib)
+    monkeypatch.setattr(F, "on_device", lambda t: contextlib.nullcontext())
+    monkeypatch.setattr(FF.R, "stream_ptr", lambda t, stream=None: 0)
+    return lib
+
+
+def block(kind=torch.float16):
+    return (on_gpu(96, 64, dtype=kind), on_gpu(96, 64, dtype=kind), on_gpu(64, 96, dtype=kind))
+
+
+def test_the_stand_ins_reach_the_library(library):
+    x, weights = on_gpu(4, 64, dtype=torch.float16), block()
+    _, saved = FF.gated_feed_forward_saved(x, *weights)
+    out = FF.gated_feed_forward_backward(x, saved, x, *weights)
+    assert len(out) == 4 and library.calls == 2
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float32, torch.float64, torch.uint8,
+                                  torch.int16])
+def test_x_and_dy_of_another_type_than_the_weights(library, kind):
+    x, dy = on_gpu(4, 64, dtype=kind), on_gpu(4, 64, dtype=kind)
+    saved, weights = torch.zeros(1 << 16, dtype=torch.uint8), block()
+    ff = F.make_ff(*weights)
+    half = on_gpu(4, 64, dtype=torch.float16)
+    for call in (lambda: FF.gated_feed_forward_backward(dy, saved, x, *weights),
+                 lambda: FF.gated_feed_forward_backward(dy, saved, half, *weights),
+                 lambda: FF.gated_feed_forward_backward(half, saved, x, *weights),
+                 lambda: FF.gated_feed_forward_saved(x, *weights),
+                 lambda: F.gptq_ff_forward(ff, x, half),
+                 lambda: F.gptq_ff_backward(ff, x, saved, dy, half)):
+        with pytest.raises(TypeError):
+            call()
+    assert library.calls == 0
