@@ -11,6 +11,7 @@ import threading
 import weakref
 
 import torch
+from torch.autograd import forward_ad
 
 from . import binding_ff as F
 from . import binding_run as R
@@ -175,11 +176,15 @@ class _GatedFeedForward(torch.autograd.Function):
 def gated_feed_forward(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
                        down: torch.Tensor) -> torch.Tensor:
     """x tokens x d -> y tokens x d; gate and up inner x d, down d x inner; all
-    float16 or all bfloat16.  Differentiable once in all four, on the current stream.
+    float16 or all bfloat16.  Differentiable once in all four, on the current stream; not in
+    forward mode.
 
     It may be captured into a CUDA graph, its backward pass too, while no graph of the same
     tensors made outside of the capture is alive (such a call of this function is
     refused; of other functions it cannot know)."""
+    if forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None
+                                              for t in (x, gate, up, down)):
+        raise NotImplementedError("gated_feed_forward has no forward-mode derivative")
     if torch.is_grad_enabled() and (x.requires_grad or gate.requires_grad or up.requires_grad or
                                     down.requires_grad):
         return _GatedFeedForward.apply(x, gate, up, down)

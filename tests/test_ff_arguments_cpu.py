@@ -69,3 +69,21 @@ def test_x_and_dy_of_another_type_than_the_weights(library, kind):
         with pytest.raises(TypeError):
             call()
     assert library.calls == 0
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_tangents(library, which):
+    """A result without one would be a derivative of zero."""
+    from torch.autograd import forward_ad
+    args = [on_gpu(4, 64, dtype=torch.float16), *block()]
+    with forward_ad.dual_level():
+        FF.gated_feed_forward(*args)
+        assert library.calls == 1
+        args[which] = forward_ad.make_dual(args[which], torch.ones_like(args[which]))
+        for mode in (torch.enable_grad, torch.no_grad):
+            with mode(), pytest.raises(NotImplementedError, match="forward-mode"):
+                FF.gated_feed_forward(*args)
+        args[which].requires_grad_()
+        with pytest.raises(NotImplementedError, match="forward-mode"):
+            FF.gated_feed_forward(*args)
+    assert library.calls == 1

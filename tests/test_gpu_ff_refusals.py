@@ -19,3 +19,17 @@ def test_x_and_dy_of_another_type_than_the_weights(t):
             FF.gated_feed_forward_backward(dy, saved, x.to(kind), gate, up, down)
         with pytest.raises(TypeError):
             FF.gated_feed_forward_saved(x.to(kind), gate, up, down)
+
+
+def test_tangents():
+    import torch
+    from torch.autograd import forward_ad
+    from post_weight_quantization_layer_amd.feed_forward import gated_feed_forward
+    args = make(62, 4, 64, 96, "bf16")[:4]
+    with forward_ad.dual_level():
+        gated_feed_forward(*args)
+        for i in range(4):
+            dual = list(args)
+            dual[i] = forward_ad.make_dual(args[i], torch.ones_like(args[i]))
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                gated_feed_forward(*dual)
