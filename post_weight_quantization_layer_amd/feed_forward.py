@@ -115,6 +115,8 @@ def gated_feed_forward_backward(dy: torch.Tensor, saved: torch.Tensor | None, x:
                                 needed=(True, True, True, True), stream=None):
     """Gradients of x, gate, up and down (None where not ``needed``) for the gradient
     ``dy`` of y.  x and the weights have to be what the forward pass had."""
+    if len(needed) != 4:
+        raise ValueError(f"needed says of four gradients whether, got {len(needed)}")
     ff = F.make_ff(gate, up, down)
     F.one_device(x, gate, up, down, dy)
     if saved is not None:

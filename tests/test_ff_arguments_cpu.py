@@ -87,3 +87,12 @@ def test_tangents(library, which):
         with pytest.raises(NotImplementedError, match="forward-mode"):
             FF.gated_feed_forward(*args)
     assert library.calls == 1
+
+
+@pytest.mark.parametrize("needed", [(), (True,), (True, True, True), (True,) * 5])
+def test_needed_names_four_gradients(library, needed):
+    x, weights = on_gpu(4, 64, dtype=torch.float16), block()
+    saved = torch.zeros(1 << 16, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="needed"):
+        FF.gated_feed_forward_backward(x, saved, x, *weights, needed)
+    assert library.calls == 0
