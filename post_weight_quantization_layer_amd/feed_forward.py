@@ -128,32 +128,55 @@ def gated_feed_forward_backward(dy: torch.Tensor, saved: torch.Tensor | None, x:
 
 
 class _Eager:
-    """Alive as long as a graph made outside of a capture, with its leaves."""
+    """Alive as long as a graph made outside of a capture, with where it goes on to its leaves."""
     living: "weakref.WeakSet[_Eager]" = weakref.WeakSet()
     lock = threading.Lock()              # a set may not grow while it is read
 
-    def __init__(self, leaves):
-        self.leaves = [weakref.ref(t) for t in leaves]
+    def __init__(self, inputs):
+        self.leaves = [weakref.ref(t) for t in inputs if t.grad_fn is None]
+        self.nodes = [t.grad_fn for t in inputs if t.grad_fn is not None]
         with self.lock:
             self.living.add(self)
 
 
-def _graph_of(leaves):
-    """A token for the graph that is being made from these leaves.
+def _leaves_below(nodes, seen: set) -> list:
+    """The leaves that the graphs below these nodes end in, without what is below ``seen``."""
+    found, stack = [], list(nodes)
+    while stack:
+        node = stack.pop()
+        if node is None or node in seen:
+            continue
+        seen.add(node)
+        leaf = getattr(node, "variable", None)
+        if isinstance(leaf, torch.Tensor):
+            found.append(leaf)
+        stack.extend(n for n, _ in node.next_functions)
+    return found
+
+
+def _graph_of(inputs):
+    """A token for the graph that is being made from these inputs.
 
     The nodes that add up a leaf's gradient belong to the stream of the first living graph
     of it.  A captured backward pass that reached nodes of another stream would make
     that stream wait for the capture, an error in a thread of autograd's that ends the
-    process; so it is refused here."""
+    process; so it is refused here.  An input may be made of leaves (a view of a packed
+    weight, a cast of a master weight, another layer's output): those count, and are looked
+    for only in a capture, where a walk costs nothing that is replayed."""
     if not R.capturing():
-        return _Eager(leaves)
+        return _Eager(inputs)
     with _Eager.lock:
         living = list(_Eager.living)
-    for graph in living:
-        if any(r() is t for r in graph.leaves for t in leaves):
-            raise RuntimeError("a graph of the same tensors made outside of this capture is alive: "
-                               "drop its outputs first, or capture gated_feed_forward_saved and "
-                               "gated_feed_forward_backward, which make none")
+    seen: set = set()
+    theirs = [t for graph in living for t in (r() for r in graph.leaves) if t is not None]
+    theirs += _leaves_below((n for graph in living for n in graph.nodes), seen)
+    ours = [t for t in inputs if t.grad_fn is None]
+    ours += _leaves_below((t.grad_fn for t in inputs), set())
+    taken = {id(t) for t in theirs}
+    if any(id(t) in taken for t in ours):
+        raise RuntimeError("a graph of the same tensors made outside of this capture is alive: "
+                           "drop its outputs first, or capture gated_feed_forward_saved and "
+                           "gated_feed_forward_backward, which make none")
     return None
 
 
@@ -181,9 +204,10 @@ def gated_feed_forward(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
     float16 or all bfloat16.  Differentiable once in all four, on the current stream; not in
     forward mode.
 
-    It may be captured into a CUDA graph, its backward pass too, while no graph of the same
-    tensors made outside of the capture is alive (such a call of this function is
-    refused; of other functions it cannot know)."""
+    It may be captured into a CUDA graph, with its backward pass in the same capture, while no
+    graph of the same tensors, or of what they are made of, that was made outside of the
+    capture is alive (such a call of this function is refused; of other functions it cannot
+    know)."""
     if forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None
                                               for t in (x, gate, up, down)):
         raise NotImplementedError("gated_feed_forward has no forward-mode derivative")

@@ -33,3 +33,51 @@ def test_tangents():
             dual[i] = forward_ad.make_dual(args[i], torch.ones_like(args[i]))
             with pytest.raises(NotImplementedError, match="forward-mode"):
                 gated_feed_forward(*dual)
+
+
+def test_a_capture_beside_a_living_graph_of_a_packed_weight():
+    import torch
+    from post_weight_quantization_layer_amd import binding_run as R
+    from post_weight_quantization_layer_amd import feed_forward as FF
+    x, gate, up, down, dy = make(63, 20, 64, 96, "bf16")
+    packed = torch.cat([gate, up]).requires_grad_()
+    master = down.float().requires_grad_()
+
+    def call():
+        return FF.gated_feed_forward(x, *packed.chunk(2), master.bfloat16())
+    y = call()
+    want = torch.autograd.grad(y, (packed, master), dy, retain_graph=True)
+    capturing = R.capturing
+    R.capturing = lambda stream=None: True       # as if; nothing is captured
+    try:
+        with pytest.raises(RuntimeError, match="alive"):
+            call()
+        with pytest.raises(RuntimeError, match="alive"):
+            FF.gated_feed_forward(y, gate, up, down)
+        del y
+        got = torch.autograd.grad(call(), (packed, master), dy)
+    finally:
+        R.capturing = capturing
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_packed_weights_captured():
+    import torch
+    from post_weight_quantization_layer_amd import feed_forward as FF
+    x, gate, up, down, dy = make(64, 40, 64, 96, "f16")
+    packed = torch.cat([gate, up]).requires_grad_()
+    y = FF.gated_feed_forward(x, *packed.chunk(2), down)
+    want = (y.detach().clone(), torch.autograd.grad(y, packed, dy)[0])
+    del y
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = FF.gated_feed_forward(x, *packed.chunk(2), down)
+        got = (y.detach(), torch.autograd.grad(y, packed, dy)[0])
+        del y
+    for _ in range(4):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
