@@ -112,7 +112,7 @@ gptq_status gptq_f8_gemm(const gptq_f8_layer *layer, const uint8_t *codes,
 
 /* The same on float activations (F32, BF16 or F16): the outputs are those of
  * gptq_f8_quantize_tokens followed by gptq_f8_gemm, bit for bit.  y may not
- * overlap x. */
+ * overlap x (other columns of one matrix do not). */
 gptq_status gptq_f8_linear(const gptq_f8_layer *layer, const void *x,
                            int32_t x_dtype, int64_t ld_x, int64_t tokens,
                            void *y, int32_t y_dtype, int64_t ld_y, void *ws,

@@ -1180,7 +1180,7 @@ gptq_status gptq_f8_linear(const gptq_f8_layer *layer, const void *x, int32_t x_
     GPTQ_TRY(check_activations(x, x_dtype, tokens, layer->cols, ld_x, "x"));
     if (tokens == 0) return GPTQ_OK;
     GPTQ_TRY(check_output(y, y_dtype, ld_y, layer->rows));
-    if (extents_meet(x, tokens, layer->cols, ld_x, type_bytes(x_dtype), y, tokens, layer->rows, ld_y,
+    if (matrices_meet(x, tokens, layer->cols, ld_x, type_bytes(x_dtype), y, tokens, layer->rows, ld_y,
                      2))
       return fail(GPTQ_ERR_INVALID_ARG, "y must not overlap x");
     GPTQ_TRY(check_scratch(ws, ws_bytes, gptq_f8_linear_ws_bytes(layer, tokens)));

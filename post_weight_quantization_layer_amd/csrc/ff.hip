@@ -839,7 +839,7 @@ struct Padder {
 
 bool overlap(const void *a, int64_t rows_a, int64_t cols_a, int64_t ld_a, const void *b,
              int64_t rows_b, int64_t cols_b, int64_t ld_b) {
-  return extents_meet(a, rows_a, cols_a, ld_a, 2, b, rows_b, cols_b, ld_b, 2);
+  return matrices_meet(a, rows_a, cols_a, ld_a, 2, b, rows_b, cols_b, ld_b, 2);
 }
 
 gptq_status check_ff(const gptq_ff *f) {

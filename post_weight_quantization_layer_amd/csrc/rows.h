@@ -39,6 +39,28 @@ inline bool is_float_type(int32_t t) {
 inline size_t type_bytes(int32_t t) { return t == GPTQ_DT_F32 ? 4 : 2; }
 inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether n rows of `width_a` bytes, `pitch_a` bytes apart from a on, and m of `width_b`,
+// `pitch_b` apart from b on, share a byte.  (Columns of one matrix do not.)
+inline bool rows_overlap(const void *a, uint64_t n, uint64_t pitch_a, uint64_t width_a, const void *b,
+                         uint64_t m, uint64_t pitch_b, uint64_t width_b) {
+  if (reinterpret_cast<uintptr_t>(a) > reinterpret_cast<uintptr_t>(b))
+    return rows_overlap(b, m, pitch_b, width_b, a, n, pitch_a, width_a);
+  const uint64_t gap = reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a);
+  if (gap >= (n - 1) * pitch_a + width_a) return false;   // b begins after a's last row
+  uint64_t i = gap / pitch_a, j = 0;                      // the row of a that b begins in
+  if (pitch_a == pitch_b) {
+    const uint64_t at = gap % pitch_a;
+    return at < width_a || (at + width_b > pitch_a && i + 1 < n);
+  }
+  while (i < n && j < m) {                                // along both, row by row
+    const uint64_t x = i * pitch_a, y = gap + j * pitch_b;
+    if (x < y + width_b && y < x + width_a) return true;
+    if (x < y) ++i;
+    else ++j;
+  }
+  return false;
+}
+
 struct f16_t {
   uint16_t bits;
 };

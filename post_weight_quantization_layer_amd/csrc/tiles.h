@@ -176,19 +176,24 @@ __device__ __forceinline__ void store_turned(V value, T *out, int64_t ld, int ro
   }
 }
 
-// Whether the extents of two matrices (rows x cols of elements of `size` bytes, ld between
-// rows) meet; false for a matrix that is not there.
-inline bool extents_meet(const void *a, int64_t rows_a, int64_t cols_a, int64_t ld_a, size_t size_a,
-                         const void *b, int64_t rows_b, int64_t cols_b, int64_t ld_b,
-                         size_t size_b) {
+// Whether two matrices (rows x cols of elements of `size` bytes, ld >= cols between rows) share
+// memory; false for a matrix that is not there.  A stride that reaches past the address
+// space counts as all that is on the way.
+inline bool matrices_meet(const void *a, int64_t rows_a, int64_t cols_a, int64_t ld_a, size_t size_a,
+                          const void *b, int64_t rows_b, int64_t cols_b, int64_t ld_b,
+                          size_t size_b) {
   if (!a || !b || rows_a < 1 || rows_b < 1) return false;
   // in 128 bits: any stride
   const auto end = [](const void *p, int64_t rows, int64_t cols, int64_t ld, size_t size) {
     return (unsigned __int128)(reinterpret_cast<uintptr_t>(p)) +
            ((unsigned __int128)(rows - 1) * uint64_t(rows > 1 ? ld : 0) + uint64_t(cols)) * size;
   };
-  return reinterpret_cast<uintptr_t>(a) < end(b, rows_b, cols_b, ld_b, size_b) &&
-         reinterpret_cast<uintptr_t>(b) < end(a, rows_a, cols_a, ld_a, size_a);
+  const unsigned __int128 end_a = end(a, rows_a, cols_a, ld_a, size_a);
+  const unsigned __int128 end_b = end(b, rows_b, cols_b, ld_b, size_b);
+  if (reinterpret_cast<uintptr_t>(a) >= end_b || reinterpret_cast<uintptr_t>(b) >= end_a) return false;
+  if (end_a > UINTPTR_MAX || end_b > UINTPTR_MAX) return true;
+  return rows_overlap(a, rows_a, (rows_a > 1 ? ld_a : cols_a) * size_a, cols_a * size_a, b, rows_b,
+                      (rows_b > 1 ? ld_b : cols_b) * size_b, cols_b * size_b);
 }
 
 inline gptq_status check_scratch(const void *ws, size_t ws_bytes, size_t need) {

@@ -81,3 +81,18 @@ def test_packed_weights_captured():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("t", [2, 40])
+def test_columns_of_one_matrix(t):
+    """x and y side by side in one matrix: the bits of separate ones, and x stays as it is."""
+    import torch
+    from post_weight_quantization_layer_amd.f8 import F8Linear
+    x, gate, *_ = make(65, t, 136, 72, "f16")
+    lin = F8Linear.from_weight(gate)
+    both = torch.full((t, 136 + 72 + 3), 5.0, dtype=x.dtype, device="cuda")
+    for at, to in ((0, 136), (72, 0)):
+        left, y = both[:, at:at + 136], both[:, to:to + 72]
+        left.copy_(x)
+        assert lin(left, y) is y
+        assert torch.equal(y, lin(x)) and torch.equal(left, x) and bool((both[:, 208:] == 5).all())
