@@ -82,6 +82,11 @@ def on_device(t: torch.Tensor):
     return torch.cuda.device(t.get_device())
 
 
+def on_index(device: torch.device):
+    """The same for a device; "cuda" is the current one."""
+    return _CURRENT if device.index is None else torch.cuda.device(device)
+
+
 def one_device(*tensors: torch.Tensor):
     device = tensors[0].get_device()
     for t in tensors:

@@ -26,7 +26,7 @@ class F8Tokens:
     def __init__(self, tokens: int, cols: int, device="cuda", stream=None):
         device = R.on_gpu(device, "token codes")
         self.tokens, self.cols = tokens, cols
-        with R.on(stream):
+        with F.on_index(device), R.on(stream):
             self.codes = torch.empty((tokens, R.gptq_tokens_ld(cols)), dtype=torch.uint8,
                                      device=device)
             self.scale = torch.empty((blocks(cols), tokens), dtype=torch.float32, device=device)
@@ -57,10 +57,11 @@ def quantize_weight(w: torch.Tensor, stream=None) -> tuple[torch.Tensor, torch.T
     if w.dim() != 2 or not w.is_cuda:
         raise ValueError("a weight must be a rows x cols matrix on the GPU")
     rows, cols = w.shape
-    with R.on(stream):
-        codes = torch.empty((rows, cols), dtype=torch.uint8, device=w.device)
-        scale = torch.empty((blocks(rows), blocks(cols)), dtype=torch.float32, device=w.device)
     with F.on_device(w):
+        with R.on(stream):
+            codes = torch.empty((rows, cols), dtype=torch.uint8, device=w.device)
+            scale = torch.empty((blocks(rows), blocks(cols)), dtype=torch.float32,
+                                device=w.device)
         F.gptq_f8_quantize_weight(w, codes, scale, stream)
     return codes.view(torch.float8_e4m3fn), scale
 
@@ -83,10 +84,10 @@ class F8Linear:
                              f"got {tuple(scale.shape)}")
         F.one_device(codes, scale)
         self.device = codes.device
-        with R.on(stream):
-            self.mem = torch.empty(F.gptq_f8_layer_bytes(self.rows, self.cols),
-                                   dtype=torch.uint8, device=self.device)
         with F.on_device(codes):
+            with R.on(stream):
+                self.mem = torch.empty(F.gptq_f8_layer_bytes(self.rows, self.cols),
+                                       dtype=torch.uint8, device=self.device)
             self.layer = F.gptq_f8_prepare(codes, scale, self.mem, stream)
         self.scratch = R.Scratch(self.device)
         self._last: dict = {}

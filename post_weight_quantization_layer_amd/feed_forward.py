@@ -100,10 +100,9 @@ def gated_feed_forward_saved(x: torch.Tensor, gate: torch.Tensor, up: torch.Tens
 
 
 def _backward(ff, dy, saved, x, gate, up, down, needed, stream=None):
-    if not dy.is_contiguous() and (dy.stride(-1) != 1 or dy.stride(0) < dy.shape[1]):
-        with R.on(stream):
-            dy = dy.contiguous()        # an expanded gradient, as that of a sum
     with F.on_device(x), R.on(stream):
+        if not dy.is_contiguous() and (dy.stride(-1) != 1 or dy.stride(0) < dy.shape[1]):
+            dy = dy.contiguous()        # an expanded gradient, as that of a sum
         out = [_new(t) if n else None for t, n in zip((x, gate, up, down), needed)]
         ws = _bytes(F.gptq_ff_backward_ws_bytes(ff, x.shape[0]), x.device)
         F.gptq_ff_backward(ff, x, saved, dy, *out, ws, stream)
