@@ -119,9 +119,9 @@ gptq_status gptq_f8_linear(const gptq_f8_layer *layer, const void *x,
                            size_t ws_bytes, void *stream);
 
 /* --------------------------------- gated feed-forward block on 8-bit floats
- *   g, u = codes(x) W_gate^T, codes(x) W_up^T     in float32
+ *   g, u = codes(x) W_gate^T, codes(x) W_up^T     in float32, every product whole
  *   v    = silu(g) u                              in float32
- *   y    = codes(v) W_down^T                      rounded to y's type
+ *   y    = codes(v) W_down^T                      as gptq_f8_gemm, rounded to y's type
  *
  * silu(g) = g / (1 + e^-g) (NaN for g = -infinity).
  */

@@ -1,5 +1,5 @@
-"""The block on 8-bit floats where few tokens meet a wide down product, whose k is split: what
-it writes stays within the scratch it asks for."""
+"""The block on 8-bit floats at its ends: few tokens of a wide block, whose down product is
+split, within the scratch that it asks for; long prompts, with sums to 32 bits."""
 import pytest
 
 from tests.test_gpu_f8 import U, block_reference, launched, make, stored
@@ -33,3 +33,24 @@ def test_few_tokens_of_a_wide_block(t, d, n):
     e = (d / 128 + 12) * 2.0 ** -24
     off = 2.0 ** -3 * (16 * e) ** 0.5 + 4e-5
     assert (y.double() - want).norm() / want.norm() <= U["f16"] + off
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("t,d,n", [(1030, 260, 8300), (2048, 1024, 4096), (2100, 4096, 5000)])
+def test_long_prompts_sum_to_32_bits(t, d, n, kind):
+    """Gate and up are held to 32 bits on the largest tiles as on the others: the tolerance of
+    test_gpu_f8's blocks for those.  In float16 it tells them from sums that lose bits."""
+    import torch
+    from post_weight_quantization_layer_amd.f8 import F8Linear
+    from post_weight_quantization_layer_amd.feed_forward import GatedFeedForwardF8
+    layers = [stored(i + d, *shape) for i, shape in enumerate(((n, d), (n, d), (d, n)))]
+    block = GatedFeedForwardF8(*(F8Linear(c, s) for c, s, _ in layers))
+    x = make(t, t, d, kind)
+    out = {}
+    names = launched(lambda: out.update(y=block(x)))
+    if torch.cuda.get_device_properties(0).multi_processor_count == 256:
+        assert "f8_gate_up_256x256" in names
+    want = block_reference(x, layers)
+    off = ((out["y"].double() - want).norm() / want.norm()).item()
+    print("of the norm", off)
+    assert off <= U[kind] + 7e-4 + 4e-5
