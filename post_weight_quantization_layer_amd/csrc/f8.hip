@@ -1,8 +1,8 @@
 // Layers of 8-bit floats (e4m3) with a scale per 128 x 128 block, on activations
 // quantized per token and 128 features: v_mfma_f32_16x16x128_f8f6f4, whose k is one
 // block, so each instruction's result is scaled by the two blocks' scales as it is
-// added to the float32 sum.  Gate and up of a block go through float16 instructions
-// where memory bounds them.
+// added to the float32 sum.  Gate and up of a block go through float16 instructions,
+// which keep every product whole.
 //
 // Prepared layout: tiles of 16 rows x 128 k as the instruction takes them, two
 // 1 KiB halves of 64 k; lane l holds row l % 16, k = 16 (l / 16) .. + 15 of
