@@ -72,8 +72,8 @@ def _new(t: torch.Tensor) -> torch.Tensor:
         torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
-def _forward(x, gate, up, down, save: bool, stream=None):
-    """(y, saved or None, ff)"""
+def _block(x, gate, up, down):
+    """The weights of a forward pass whose arguments fit."""
     kind = x.dtype
     if kind is not gate.dtype:
         raise TypeError(f"x and the weights must be of one type, got {kind} and {gate.dtype}")
@@ -82,13 +82,18 @@ def _forward(x, gate, up, down, save: bool, stream=None):
     ff = F.make_ff(gate, up, down)
     R.matrix(x, "x", None, ff.d)
     F.one_device(x, gate, up, down)
+    return ff
+
+
+def _forward(ff, x, save: bool, stream=None):
+    """(y, saved or None)"""
     t = x.shape[0]
     with F.on_device(x), R.on(stream):
         y = _new(x)
         saved = _bytes(F.gptq_ff_saved_bytes(ff, t), x.device) if save else None
         ws = _bytes(F.gptq_ff_forward_ws_bytes(ff, t), x.device)
         F.gptq_ff_forward(ff, x, y, saved, ws, stream)
-    return y, saved, ff
+    return y, saved
 
 
 def gated_feed_forward_saved(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
@@ -96,7 +101,7 @@ def gated_feed_forward_saved(x: torch.Tensor, gate: torch.Tensor, up: torch.Tens
     """(y, saved): the forward pass with what ``gated_feed_forward_backward`` takes (an
     opaque byte tensor, None for no tokens), outside of autograd."""
     with torch.no_grad():
-        return _forward(x, gate, up, down, True, stream)[:2]
+        return _forward(_block(x, gate, up, down), x, True, stream)
 
 
 def _backward(ff, dy, saved, x, gate, up, down, needed, stream=None):
@@ -182,8 +187,10 @@ def _graph_of(inputs):
 class _GatedFeedForward(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, gate, up, down):
-        ctx.graph = _graph_of([t for t in (x, gate, up, down) if t.requires_grad])
-        y, saved, ctx.ff = _forward(x, gate, up, down, True)
+        ctx.ff = _block(x, gate, up, down)
+        with F.on_device(x):
+            ctx.graph = _graph_of([t for t in (x, gate, up, down) if t.requires_grad])
+        y, saved = _forward(ctx.ff, x, True)
         ctx.save_for_backward(x, gate, up, down, saved)
         return y
 
@@ -213,4 +220,4 @@ def gated_feed_forward(x: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
     if torch.is_grad_enabled() and (x.requires_grad or gate.requires_grad or up.requires_grad or
                                     down.requires_grad):
         return _GatedFeedForward.apply(x, gate, up, down)
-    return _forward(x, gate, up, down, False)[0]
+    return _forward(_block(x, gate, up, down), x, False)[0]

@@ -96,3 +96,29 @@ def test_needed_names_four_gradients(library, needed):
     with pytest.raises(ValueError, match="needed"):
         FF.gated_feed_forward_backward(x, saved, x, *weights, needed)
     assert library.calls == 0
+
+
+def test_tensors_on_the_cpu_with_and_without_gradients():
+    """The arguments are looked at before the GPU is."""
+    for needs in (False, True):
+        args = [torch.zeros(s, dtype=torch.float16, requires_grad=needs)
+                for s in ((4, 64), (96, 64), (96, 64), (64, 96))]
+        with pytest.raises(ValueError, match="on the GPU"):
+            FF.gated_feed_forward(*args)
+        with pytest.raises(TypeError, match="one type"):
+            FF.gated_feed_forward(args[0].double(), *args[1:])
+
+
+def test_a_capture_is_looked_for_on_the_tensors_device(library, monkeypatch):
+    current = []
+
+    @contextlib.contextmanager
+    def on_device(t):
+        current.append(True)
+        yield
+        current.pop()
+    asked = []
+    monkeypatch.setattr(F, "on_device", on_device)
+    monkeypatch.setattr(FF.R, "capturing", lambda: asked.append(bool(current)))
+    FF.gated_feed_forward(on_gpu(4, 64, dtype=torch.float16).requires_grad_(), *block())
+    assert asked == [True] and library.calls == 1
